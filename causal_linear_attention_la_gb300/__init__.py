@@ -36,12 +36,17 @@ __all__ = [
     "forward", "decode_step", "decode_steps", "backward",
     "decode_steps_decay", "decode_steps_delta", "state_copy", "forward_decay",
     "la_forward_delta", "forward_delta", "la_forward_plan", "forward_plan",
+    "LA_TREE_MAX", "la_decode_tree", "la_decode_tree_delta", "la_verify_chain", "la_verify_tree",
+    "la_state_advance", "la_state_advance_delta", "la_state_pack", "la_state_unpack",
+    "decode_tree", "decode_tree_delta", "verify_chain", "verify_tree",
+    "state_advance", "state_advance_delta", "state_pack", "state_unpack", "state_pool",
 ]
 
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_TIMEOUT = range(5)
 LA_F32, LA_BF16 = 0, 1
 LA_PATH_AUTO, LA_PATH_SIMT = 0, 1
 LA_NOALLOC_SCRATCH_BYTES = 16 << 20   # include/la.h
+LA_TREE_MAX = 64                      # include/la.h
 SPAN_NAMES = ("fwd_state", "fwd_scan", "fwd_output", "decode", "bwd_state",
               "bwd_sweep1", "bwd_scan", "bwd_sweep2")
 
@@ -56,6 +61,8 @@ exported_symbols = (
     "la_device_status", "la_test_timeout_next_forward", "la_forward_noalloc",
     "la_forward_host_workspace_size", "la_forward_host", "la_backward_saved",
     "la_backward_decay", "la_forward_delta", "la_forward_plan",
+    "la_decode_tree", "la_decode_tree_delta", "la_verify_chain", "la_verify_tree",
+    "la_state_advance", "la_state_advance_delta", "la_state_pack", "la_state_unpack",
 )
 
 
@@ -125,6 +132,22 @@ def lib():
         [_c_void] * 3 + [ctypes.c_size_t, _c_void]
     h.la_state_copy.restype = _c_int
     h.la_state_copy.argtypes = [_c_void] * 4 + [_c_int] * 4 + [_c_void]
+    h.la_decode_tree.restype = _c_int
+    h.la_decode_tree.argtypes = [_c_void] * 8 + [_c_int] * 5 + [_c_void, _c_float, _c_int, _c_void]
+    h.la_decode_tree_delta.restype = _c_int
+    h.la_decode_tree_delta.argtypes = [_c_void] * 7 + [_c_int] * 6 + [_c_void]
+    h.la_verify_chain.restype = _c_int
+    h.la_verify_chain.argtypes = [_c_void] * 7 + [_c_int] * 4 + [_c_void]
+    h.la_verify_tree.restype = _c_int
+    h.la_verify_tree.argtypes = [_c_void] * 8 + [_c_int] * 4 + [_c_void]
+    h.la_state_advance.restype = _c_int
+    h.la_state_advance.argtypes = [_c_void] * 8 + [_c_int] * 5 + [_c_void, _c_int, _c_void]
+    h.la_state_advance_delta.restype = _c_int
+    h.la_state_advance_delta.argtypes = [_c_void] * 6 + [_c_int] * 6 + [_c_void]
+    h.la_state_pack.restype = _c_int
+    h.la_state_pack.argtypes = [_c_void] * 6 + [_c_int] * 5 + [_c_void]
+    h.la_state_unpack.restype = _c_int
+    h.la_state_unpack.argtypes = [_c_void] * 6 + [_c_int] * 5 + [_c_void]
     h.la_backward.restype = _c_int
     h.la_backward.argtypes = ([_c_void] * 7 + [_c_int] * 6 + [_c_float, _c_int]
                               + [_c_void, _c_size, _c_void])
@@ -257,6 +280,39 @@ def la_backward(q, k, v, dout, dq, dk_, dv_, B, H, N, dk, dv, causal, eps,
     return lib().la_backward(q, k, v, dout, dq, dk_, dv_, B, H, N, dk, dv,
                              int(causal), eps, dtype, workspace,
                              workspace_bytes, stream)
+
+
+def la_decode_tree(S, z, q, k, v, parent, count, out, B, H, T, dk, dv, alpha, eps, dtype, stream):
+    return lib().la_decode_tree(S, z, q, k, v, parent, count, out, B, H, T, dk, dv, alpha, eps, dtype, stream)
+
+
+def la_decode_tree_delta(S, q, k, v, parent, count, out, B, H, T, dk, dv, dtype, stream):
+    return lib().la_decode_tree_delta(S, q, k, v, parent, count, out, B, H, T, dk, dv, dtype, stream)
+
+
+def la_verify_chain(target, draft, tokens, count, uniform, accepted, next, B, T, V, dtype, stream):
+    return lib().la_verify_chain(target, draft, tokens, count, uniform, accepted, next, B, T, V, dtype, stream)
+
+
+def la_verify_tree(target, tokens, parent, count, uniform, path, accepted, next, B, T, V, dtype, stream):
+    return lib().la_verify_tree(target, tokens, parent, count, uniform, path, accepted, next, B, T, V, dtype,
+                                stream)
+
+
+def la_state_advance(S, z, k, v, path, accepted, S_out, z_out, B, H, T, dk, dv, alpha, dtype, stream):
+    return lib().la_state_advance(S, z, k, v, path, accepted, S_out, z_out, B, H, T, dk, dv, alpha, dtype, stream)
+
+
+def la_state_advance_delta(S, k, v, path, accepted, S_out, B, H, T, dk, dv, dtype, stream):
+    return lib().la_state_advance_delta(S, k, v, path, accepted, S_out, B, H, T, dk, dv, dtype, stream)
+
+
+def la_state_pack(S, z, codes, scales, z_pool, slot, B, H, dk, dv, slots, stream):
+    return lib().la_state_pack(S, z, codes, scales, z_pool, slot, B, H, dk, dv, slots, stream)
+
+
+def la_state_unpack(codes, scales, z_pool, slot, S, z, B, H, dk, dv, slots, stream):
+    return lib().la_state_unpack(codes, scales, z_pool, slot, S, z, B, H, dk, dv, slots, stream)
 
 
 def la_set_path(path):
@@ -583,3 +639,206 @@ def backward_saved(q, k, v, dout, saved, causal=True, eps=1e-6, workspace=None):
                              dk, dv, causal, eps, code, saved.data_ptr(), saved.numel(),
                              workspace.data_ptr(), workspace.numel(), _stream_ptr(q)))
     return dq, dkk, dvv
+
+
+# ---------------------------------------------------------------------------
+# Speculative decoding: drafted trees and chains on the recurrent state
+# ---------------------------------------------------------------------------
+
+
+def _need_like(device, **tensors):
+    """Each value is (tensor, dtype, shape): contiguous, on ``device``, of that
+    dtype and shape (None tensors pass)."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _shape4(t, name):
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return tuple(t.shape)
+
+
+def _on(device, call, *args):
+    """call(*args, stream) with ``device`` current, on its current stream."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        _check(call(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def decode_tree(S, z, q, k, v, parent, alpha=None, eps=1e-6, count=None, out=None):
+    """Outputs [B,H,T,dv] of every node of a drafted tree read against the
+    fp32 state S [B,H,dk,dv], z [B,H,dk], which is not changed (la_decode_tree).
+
+    q, k [B,H,T,dk], v [B,H,T,dv] (bf16 or f32), T <= LA_TREE_MAX; parent [B,T]
+    int32, -1 or an earlier node; alpha [H] f32: decay per head; count [B]
+    int32: nodes of each sequence, rows of ``out`` behind them are left as they
+    are (zero where ``out`` is allocated here).
+    """
+    import torch
+    B, H, dk, dv = _shape4(S, "S")
+    T = _shape4(q, "q")[2]
+    dev, f32, i32 = S.device, torch.float32, torch.int32
+    code = _dtype_code(q)
+    if out is None:
+        out = (torch.empty if count is None else torch.zeros)((B, H, T, dv), dtype=q.dtype, device=dev)
+    _need_like(dev, S=(S, f32, (B, H, dk, dv)), z=(z, f32, (B, H, dk)), q=(q, q.dtype, (B, H, T, dk)),
+               k=(k, q.dtype, (B, H, T, dk)), v=(v, q.dtype, (B, H, T, dv)), parent=(parent, i32, (B, T)),
+               alpha=(alpha, f32, (H,)), count=(count, i32, (B,)), out=(out, q.dtype, (B, H, T, dv)))
+    _on(dev, la_decode_tree, S.data_ptr(), z.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        parent.data_ptr(), _ptr(count), out.data_ptr(), B, H, T, dk, dv, _ptr(alpha), eps, code)
+    return out
+
+
+def decode_tree_delta(S, q, k, v, parent, count=None, out=None):
+    """decode_tree by the delta rule (la_decode_tree_delta): q and k as given,
+    no normaliser."""
+    import torch
+    B, H, dk, dv = _shape4(S, "S")
+    T = _shape4(q, "q")[2]
+    dev, f32, i32 = S.device, torch.float32, torch.int32
+    code = _dtype_code(q)
+    if out is None:
+        out = (torch.empty if count is None else torch.zeros)((B, H, T, dv), dtype=q.dtype, device=dev)
+    _need_like(dev, S=(S, f32, (B, H, dk, dv)), q=(q, q.dtype, (B, H, T, dk)), k=(k, q.dtype, (B, H, T, dk)),
+               v=(v, q.dtype, (B, H, T, dv)), parent=(parent, i32, (B, T)), count=(count, i32, (B,)),
+               out=(out, q.dtype, (B, H, T, dv)))
+    _on(dev, la_decode_tree_delta, S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), parent.data_ptr(),
+        _ptr(count), out.data_ptr(), B, H, T, dk, dv, code)
+    return out
+
+
+def verify_chain(target, draft, tokens, uniform, count=None):
+    """(accepted [B], next [B]) int32 of drafted chains (la_verify_chain):
+    target [B,T+1,V] and draft [B,T,V] probabilities (bf16 or f32), tokens [B,T]
+    int32, uniform [B,T+1] f32 in [0, 1), count [B] int32 tokens of each."""
+    import torch
+    if target.dim() != 3 or target.shape[1] < 1 or not target.is_cuda:
+        raise ValueError("target must be a CUDA tensor [B,T+1,V]")
+    B, T, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    dev, i32 = target.device, torch.int32
+    code = _dtype_code(target)
+    _need_like(dev, target=(target, target.dtype, (B, T + 1, V)), draft=(draft, target.dtype, (B, T, V)),
+               tokens=(tokens, i32, (B, T)), uniform=(uniform, torch.float32, (B, T + 1)), count=(count, i32, (B,)))
+    got = torch.empty((2, B), dtype=i32, device=dev)
+    accepted, nxt = got[0], got[1]
+    _on(dev, la_verify_chain, target.data_ptr(), draft.data_ptr(), tokens.data_ptr(), _ptr(count),
+        uniform.data_ptr(), accepted.data_ptr(), nxt.data_ptr(), B, T, V, code)
+    return accepted, nxt
+
+
+def verify_tree(target, tokens, parent, uniform, count=None):
+    """(path [B,T], accepted [B], next [B]) int32 of drafted trees
+    (la_verify_tree): target [B,T+1,V] probabilities (bf16 or f32; row 0 after
+    the committed state, row i + 1 after node i), tokens and parent [B,T] int32,
+    uniform [B,T+1] f32 in [0, 1), count [B] int32 nodes of each."""
+    import torch
+    if target.dim() != 3 or target.shape[1] < 1 or not target.is_cuda:
+        raise ValueError("target must be a CUDA tensor [B,T+1,V]")
+    B, T, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    dev, i32 = target.device, torch.int32
+    code = _dtype_code(target)
+    _need_like(dev, target=(target, target.dtype, (B, T + 1, V)), tokens=(tokens, i32, (B, T)),
+               parent=(parent, i32, (B, T)), uniform=(uniform, torch.float32, (B, T + 1)), count=(count, i32, (B,)))
+    got = torch.empty((B * (T + 2),), dtype=i32, device=dev)
+    path, accepted, nxt = got[2 * B:].view(B, T), got[:B], got[B:2 * B]
+    _on(dev, la_verify_tree, target.data_ptr(), tokens.data_ptr(), parent.data_ptr(), _ptr(count),
+        uniform.data_ptr(), path.data_ptr(), accepted.data_ptr(), nxt.data_ptr(), B, T, V, code)
+    return path, accepted, nxt
+
+
+def state_advance(S, z, k, v, path=None, accepted=None, alpha=None, S_out=None, z_out=None):
+    """Moves each sequence's state along its accepted tokens (la_state_advance)
+    and returns (S_out, z_out): S and z themselves, in place, unless both are
+    given. k [B,H,T,dk], v [B,H,T,dv]: rows of the drafted tokens; path [B,T]
+    int32 rows in order (None: 0, 1, ...), accepted [B] int32 how many of them
+    (None: T), alpha [H] f32 decay."""
+    import torch
+    B, H, dk, dv = _shape4(S, "S")
+    T = _shape4(k, "k")[2]
+    dev, f32, i32 = S.device, torch.float32, torch.int32
+    code = _dtype_code(k)
+    if (S_out is None) != (z_out is None):
+        raise ValueError("S_out and z_out must be both given or both None")
+    if S_out is None:
+        S_out, z_out = S, z
+    _need_like(dev, S=(S, f32, (B, H, dk, dv)), z=(z, f32, (B, H, dk)), k=(k, k.dtype, (B, H, T, dk)),
+               v=(v, k.dtype, (B, H, T, dv)), path=(path, i32, (B, T)), accepted=(accepted, i32, (B,)),
+               alpha=(alpha, f32, (H,)), S_out=(S_out, f32, (B, H, dk, dv)), z_out=(z_out, f32, (B, H, dk)))
+    _on(dev, la_state_advance, S.data_ptr(), z.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(path), _ptr(accepted),
+        S_out.data_ptr(), z_out.data_ptr(), B, H, T, dk, dv, _ptr(alpha), code)
+    return S_out, z_out
+
+
+def state_advance_delta(S, k, v, path=None, accepted=None, S_out=None):
+    """state_advance by the delta rule (la_state_advance_delta); returns S_out."""
+    import torch
+    B, H, dk, dv = _shape4(S, "S")
+    T = _shape4(k, "k")[2]
+    dev, f32, i32 = S.device, torch.float32, torch.int32
+    code = _dtype_code(k)
+    if S_out is None:
+        S_out = S
+    _need_like(dev, S=(S, f32, (B, H, dk, dv)), k=(k, k.dtype, (B, H, T, dk)), v=(v, k.dtype, (B, H, T, dv)),
+               path=(path, i32, (B, T)), accepted=(accepted, i32, (B,)), S_out=(S_out, f32, (B, H, dk, dv)))
+    _on(dev, la_state_advance_delta, S.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(path), _ptr(accepted),
+        S_out.data_ptr(), B, H, T, dk, dv, code)
+    return S_out
+
+
+def state_pool(slots, H, dk, dv, device="cuda"):
+    """Empty (zero) codes, scales and z_pool tensors for ``slots`` packed states."""
+    import torch
+    w = min(32, dv)
+    return (torch.zeros((slots, H, dk, dv), dtype=torch.uint8, device=device),
+            torch.zeros((slots, H, dk, dv // w), dtype=torch.uint8, device=device),
+            torch.zeros((slots, H, dk), dtype=torch.float32, device=device))
+
+
+def _pool_args(S, z, codes, scales, z_pool, slot):
+    import torch
+    B, H, dk, dv = _shape4(S, "S")
+    slots = _shape4(codes, "codes")[0]
+    f32, u8 = torch.float32, torch.uint8
+    if (z is None) != (z_pool is None):
+        raise ValueError("z and z_pool must be both given or both None")
+    _need_like(S.device, S=(S, f32, (B, H, dk, dv)), z=(z, f32, (B, H, dk)), codes=(codes, u8, (slots, H, dk, dv)),
+               scales=(scales, u8, (slots, H, dk, dv // min(32, dv) if dv else 0)), z_pool=(z_pool, f32, (slots, H, dk)),
+               slot=(slot, torch.int32, (B,)))
+    return B, H, dk, dv, slots
+
+
+def state_pack(S, codes, scales, slot, z=None, z_pool=None):
+    """Packs the states S [B,H,dk,dv] (and z [B,H,dk]) into slots ``slot`` [B]
+    int32 of a pool (state_pool): 8-bit codes with a power-of-two scale per
+    block of min(32, dv) values (la_state_pack)."""
+    B, H, dk, dv, slots = _pool_args(S, z, codes, scales, z_pool, slot)
+    _on(S.device, la_state_pack, S.data_ptr(), _ptr(z), codes.data_ptr(), scales.data_ptr(), _ptr(z_pool),
+        slot.data_ptr(), B, H, dk, dv, slots)
+
+
+def state_unpack(codes, scales, slot, S, z_pool=None, z=None):
+    """The states of slots ``slot`` [B] int32 back into S [B,H,dk,dv] (and z)
+    (la_state_unpack); sequences whose slot is outside the pool keep theirs."""
+    B, H, dk, dv, slots = _pool_args(S, z, codes, scales, z_pool, slot)
+    _on(S.device, la_state_unpack, codes.data_ptr(), scales.data_ptr(), _ptr(z_pool), slot.data_ptr(),
+        S.data_ptr(), _ptr(z), B, H, dk, dv, slots)
+    return S

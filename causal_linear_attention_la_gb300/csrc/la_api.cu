@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "la_internal.cuh"
+#include "la_spec.cuh"
 #include "la_variants.cuh"
 
 namespace la {
@@ -175,6 +176,8 @@ int* device_status_ptr() {
   }
   return cache[dev];
 }
+
+int current_path() { return g_path.load(); }
 
 bool take_timeout_test() { return g_timeout_test.exchange(0) != 0; }
 

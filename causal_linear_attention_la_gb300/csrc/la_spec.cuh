@@ -1,0 +1,57 @@
+// Internal declarations of the speculative-decoding operators: tree decode,
+// draft verification, state advance and the packed state pool.
+#pragma once
+
+#include "la_internal.cuh"
+
+namespace la {
+
+constexpr int kTreeMax = 64;   // nodes per tree (LA_TREE_MAX): one 64-bit ancestor mask each
+
+struct TreeArgs {
+  const float* S; const float* z;            // z null: delta rule
+  const void* q; const void* k; const void* v;
+  const int* parent; const int* count;       // count null: T nodes everywhere
+  void* out;
+  int BH, H, T, dk, dv;
+  const float* alpha;                        // null: no decay
+  float eps; la_dtype dtype;
+  cudaStream_t stream;
+};
+
+struct AdvanceArgs {
+  const float* S; const float* z; float* S_out; float* z_out;   // z null: delta rule
+  const void* k; const void* v;
+  const int* path; const int* accepted;      // null: rows 0, 1, ...; null: T tokens
+  int BH, H, T, dk, dv;
+  const float* alpha; la_dtype dtype;
+  cudaStream_t stream;
+};
+
+struct VerifyArgs {
+  const void* target; const void* draft;     // draft null: tree form
+  const int* tokens; const int* parent; const int* count;
+  const float* uniform;
+  int* path; int* accepted; int* next;       // path: tree form only
+  int B, T, V; la_dtype dtype;
+  cudaStream_t stream;
+};
+
+struct PackArgs {
+  float* S; float* z;                        // z null: none stored
+  unsigned char* codes; unsigned char* scales; float* z_pool;
+  const int* slot;
+  int B, H, dk, dv, slots;
+  cudaStream_t stream;
+};
+
+cudaError_t simt_tree(const TreeArgs& a);
+cudaError_t state_advance(const AdvanceArgs& a);
+cudaError_t verify(const VerifyArgs& a);
+cudaError_t state_pack(const PackArgs& a);
+cudaError_t state_unpack(const PackArgs& a);
+
+// The current la_set_path setting.
+int current_path();
+
+}  // namespace la

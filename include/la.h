@@ -323,6 +323,165 @@ LA_API la_status la_state_copy(float* dst_S, float* dst_z, const float* src_S,
                         la_stream_t stream);
 
 /*
+ * Speculative decoding
+ * --------------------
+ * Drafted tokens are read against the committed state (la_decode_tree),
+ * checked against the target's probabilities (la_verify_chain,
+ * la_verify_tree), and the state moves along the ones that stand
+ * (la_state_advance). None of the calls needs a workspace, keeps anything
+ * between calls or uses atomics: results repeat bit for bit, and calls on
+ * different streams do not meet. int arrays are device memory, 4-byte
+ * aligned; what they hold cannot be checked without waiting for the GPU, so
+ * each entry point says what an entry out of range does (no access leaves the
+ * caller's arrays).
+ */
+
+/* Most nodes of a drafted tree, or tokens of a drafted chain. */
+#define LA_TREE_MAX 64
+
+/*
+ * Tree decode: the outputs of every node of a drafted tree, each as if
+ * la_decode_steps (la_decode_steps_decay with alpha) had run along the node's
+ * path from the committed state; S and z are read, not written:
+ *
+ *   out_i = num_i / den_i over the path anc(i) = root .. i, depth d_i = |anc(i)|
+ *   num_i = a^d_i S^T phi(q_i) + sum_{j in anc(i)} a^(d_i-d_j) (phi(q_i).phi(k_j)) v_j
+ *   den_i = a^d_i z.phi(q_i) + sum_{j in anc(i)} a^(d_i-d_j) phi(q_i).phi(k_j) + eps
+ *
+ * ("Linear Attention: KV를 고정 크기 상태에 누적하기", section "상태 갱신과 읽기를
+ * 식으로 정리하기"; the ancestor mask takes the place of the causal one).
+ *
+ * S [B,H,dk,dv], z [B,H,dk] fp32 in; q, k [B,H,T,dk], v [B,H,T,dv] in, out
+ * [B,H,T,dv] out (must not alias the inputs), dtype; alpha [H] fp32 or NULL
+ * (no decay; then a = 1).
+ * parent [B,T]: node i's parent, a node before it (parent < i), or -1 for a
+ *        child of the committed state. Any other value counts as -1.
+ * count  [B] or NULL: nodes 0 .. count[b]-1 of sequence b exist (clamped to
+ *        0 .. T); the rows behind them are neither read nor written. NULL: T.
+ * T <= LA_TREE_MAX (LA_ERR_UNSUPPORTED above); T = 0 is a no-op.
+ * A node off a path never reaches its outputs, whatever its rows hold
+ * (infinities and NaN included). fp32 arithmetic.
+ */
+LA_API la_status la_decode_tree(const float* S, const float* z, const void* q, const void* k, const void* v,
+                                const int* parent, const int* count, void* out, int B, int H, int T, int dk,
+                                int dv, const float* alpha, float eps, la_dtype dtype, la_stream_t stream);
+
+/*
+ * Tree decode by the delta rule: every node's output as if
+ * la_decode_steps_delta had run along its path; S is read, not written. The
+ * increments along the paths solve one unit lower-triangular system,
+ *   u_j = v_j - S^T k_j - sum_{l in anc(j), l != j} (k_j.k_l) u_l,
+ *   out_i = S^T q_i + sum_{j in anc(i)} (q_i.k_j) u_j.
+ * Arguments as la_decode_tree without z, alpha and eps.
+ */
+LA_API la_status la_decode_tree_delta(const float* S, const void* q, const void* k, const void* v,
+                                      const int* parent, const int* count, void* out, int B, int H, int T,
+                                      int dk, int dv, la_dtype dtype, la_stream_t stream);
+
+/*
+ * Verification of a drafted chain: token i, drawn by the draft from its own
+ * distribution q_i, stands if all before it stand and
+ *   uniform_i * q_i(x_i) < p_i(x_i)
+ * (probability min(1, p_i(x_i) / q_i(x_i)) for uniform random numbers); the
+ * token after the n that stand is drawn with uniform_T from max(p_n - q_n, 0)
+ * if one fell (from p_n if that is zero everywhere), from p_n if none did. The
+ * accepted tokens and the next one are then distributed as the target's.
+ *
+ * target   [B,T+1,V] dtype: target probabilities after 0 .. T drafted tokens
+ * draft    [B,T,V]   dtype: the distributions that tokens 0 .. T-1 were drawn from
+ * tokens   [B,T]: the drafted tokens; one outside 0 .. V-1 falls
+ * count    [B] or NULL: drafted tokens of each sequence (clamped to 0 .. T);
+ *          rows and random numbers of later ones are not used. NULL: T.
+ * uniform  [B,T+1] fp32 random numbers in [0, 1): one for each token's test,
+ *          uniform[b][T] for the draw
+ * accepted [B] out: n          next [B] out: the token after them
+ *
+ * A draw with u takes the smallest t whose weights 0 .. t sum to more than u
+ * times all of them (the last positive weight where rounding leaves none).
+ * Weights need not be normalised; those that are not above zero (NaN too) are
+ * zero. A row with no positive weight, or an infinite one, gives next = -1.
+ * Sums carry about 48 bits. T <= LA_TREE_MAX; T = 0 just draws (draft and
+ * tokens may be NULL); 1 <= V <= 2^30. target and draft 16-byte aligned.
+ */
+LA_API la_status la_verify_chain(const void* target, const void* draft, const int* tokens, const int* count,
+                                 const float* uniform, int* accepted, int* next, int B, int T, int V,
+                                 la_dtype dtype, la_stream_t stream);
+
+/*
+ * Verification of a drafted tree: from the committed state down, a token is
+ * drawn from the target's probabilities at the current context with that
+ * context's random number (the draw of la_verify_chain); the first child that
+ * holds it is accepted and becomes the context, otherwise the walk ends with
+ * it. Every token is thus a sample of the target's, whatever drafted the tree.
+ *
+ * target   [B,T+1,V] dtype: row 0 after the committed state, row i + 1 after node i
+ * tokens, parent [B,T], count [B] or NULL: the tree, as in la_decode_tree
+ * uniform  [B,T+1] fp32 in [0, 1): one for each context (row of target)
+ * path     [B,T] out: the accepted nodes from the top, then -1
+ * accepted [B] out: how many            next [B] out: the token after them
+ *
+ * Only the rows on the accepted path are read. Limits, draw and zero rows as
+ * la_verify_chain; T = 0: tokens, parent and path may be NULL.
+ */
+LA_API la_status la_verify_tree(const void* target, const int* tokens, const int* parent, const int* count,
+                                const float* uniform, int* path, int* accepted, int* next, int B, int T,
+                                int V, la_dtype dtype, la_stream_t stream);
+
+/*
+ * State advance: each sequence's state moves along its own accepted tokens,
+ *   S <- a S + phi(k_j) v_j^T, z <- a z + phi(k_j)   over j = path[b][0], path[b][1], ...
+ * as la_decode_steps (with alpha la_decode_steps_decay) would, without a read.
+ *
+ * S, z     [B,H,dk,dv], [B,H,dk] fp32 in; S_out, z_out fp32 out: S and z
+ *          themselves (in place) or other memory that does not overlap them,
+ *          both alike
+ * k, v     [B,H,T,dk], [B,H,T,dv] in, dtype: the rows of the drafted tokens
+ * path     [B,T] or NULL: rows in order, repeats allowed; an entry outside
+ *          0 .. T-1 ends the path. NULL: rows 0, 1, 2, ... (a chain)
+ * accepted [B] or NULL: tokens of each sequence (clamped to 0 .. T). NULL: T
+ * alpha    [H] fp32 or NULL: no decay
+ * A sequence without tokens keeps its state: untouched in place, else copied.
+ * Any T >= 0. fp32 arithmetic, token by token.
+ */
+LA_API la_status la_state_advance(const float* S, const float* z, const void* k, const void* v,
+                                  const int* path, const int* accepted, float* S_out, float* z_out, int B,
+                                  int H, int T, int dk, int dv, const float* alpha, la_dtype dtype,
+                                  la_stream_t stream);
+
+/* State advance by the delta rule (u = S^T k_j, S <- S + k_j (v_j - u)^T, as
+ * la_decode_steps_delta); arguments as la_state_advance without z and alpha. */
+LA_API la_status la_state_advance_delta(const float* S, const void* k, const void* v, const int* path,
+                                        const int* accepted, float* S_out, int B, int H, int T, int dk,
+                                        int dv, la_dtype dtype, la_stream_t stream);
+
+/*
+ * Packed state pool: the states of B sequences into slots of 8-bit codes
+ * (about a quarter of the fp32 bytes; prefix caching), and back.
+ *
+ * codes  [slots,H,dk,dv]: e4m3 codes; scales [slots,H,dk,dv/min(32,dv)]: one
+ *        power of two for each block of min(32, dv) values of a state row,
+ *        2^(byte - 127), the smallest (2^-127 at least) that brings the
+ *        block's largest finite magnitude to 448 or less. code = e4m3(x /
+ *        scale) to nearest, ties to even: off by at most 2^-4 of the value or
+ *        2^-10 scales, whichever is more. NaN is kept, infinities take the
+ *        largest code (with the largest scale, 2^120, codes stop at 240, so
+ *        that every finite value comes back finite).
+ * z_pool [slots,H,dk] fp32, or NULL with z NULL: z is stored as it is.
+ * slot   [B]: sequence b's slot. Outside 0 .. slots-1 the sequence is left
+ *        out (pack stores nothing, unpack leaves S and z of b as they were).
+ *        Several sequences may be unpacked from one slot; where several are
+ *        packed into one, the last of them is what it holds.
+ * The way back is exact, and packing an unpacked state again changes no value.
+ * S, z, codes, z_pool 16-byte aligned, not overlapping. H*dk*dv <= 2^30.
+ */
+LA_API la_status la_state_pack(const float* S, const float* z, unsigned char* codes, unsigned char* scales,
+                               float* z_pool, const int* slot, int B, int H, int dk, int dv, int slots,
+                               la_stream_t stream);
+LA_API la_status la_state_unpack(const unsigned char* codes, const unsigned char* scales, const float* z_pool,
+                                 const int* slot, float* S, float* z, int B, int H, int dk, int dv, int slots,
+                                 la_stream_t stream);
+
+/*
  * Bytes of scratch memory la_backward needs (0 if none): one fp32 state and
  * one fp32 reverse accumulator (dk*dv + dk each) per (batch, head, segment)
  * plus two fp32 scalars per token (the denominator and the normaliser's
