@@ -36,7 +36,7 @@ __all__ = [
     "forward", "decode_step", "decode_steps", "backward",
     "decode_steps_decay", "decode_steps_delta", "state_copy", "forward_decay",
     "la_forward_delta", "forward_delta", "la_forward_plan", "forward_plan",
-    "LA_TREE_MAX", "la_decode_tree", "la_decode_tree_delta", "la_verify_chain", "la_verify_tree",
+    "LA_TREE_MAX", "la_decode_tree", "la_decode_tree_delta", "la_tree_path", "la_verify_chain", "la_verify_tree",
     "la_state_advance", "la_state_advance_delta", "la_state_pack", "la_state_unpack",
     "decode_tree", "decode_tree_delta", "verify_chain", "verify_tree",
     "state_advance", "state_advance_delta", "state_pack", "state_unpack", "state_pool",
@@ -61,7 +61,7 @@ exported_symbols = (
     "la_device_status", "la_test_timeout_next_forward", "la_forward_noalloc",
     "la_forward_host_workspace_size", "la_forward_host", "la_backward_saved",
     "la_backward_decay", "la_forward_delta", "la_forward_plan",
-    "la_decode_tree", "la_decode_tree_delta", "la_verify_chain", "la_verify_tree",
+    "la_decode_tree", "la_decode_tree_delta", "la_tree_path", "la_verify_chain", "la_verify_tree",
     "la_state_advance", "la_state_advance_delta", "la_state_pack", "la_state_unpack",
 )
 
@@ -136,6 +136,8 @@ def lib():
     h.la_decode_tree.argtypes = [_c_void] * 8 + [_c_int] * 5 + [_c_void, _c_float, _c_int, _c_void]
     h.la_decode_tree_delta.restype = _c_int
     h.la_decode_tree_delta.argtypes = [_c_void] * 7 + [_c_int] * 6 + [_c_void]
+    h.la_tree_path.restype = _c_int
+    h.la_tree_path.argtypes = [_c_int] * 3
     h.la_verify_chain.restype = _c_int
     h.la_verify_chain.argtypes = [_c_void] * 7 + [_c_int] * 4 + [_c_void]
     h.la_verify_tree.restype = _c_int
@@ -288,6 +290,10 @@ def la_decode_tree(S, z, q, k, v, parent, count, out, B, H, T, dk, dv, alpha, ep
 
 def la_decode_tree_delta(S, q, k, v, parent, count, out, B, H, T, dk, dv, dtype, stream):
     return lib().la_decode_tree_delta(S, q, k, v, parent, count, out, B, H, T, dk, dv, dtype, stream)
+
+
+def la_tree_path(dk, dv, dtype):
+    return lib().la_tree_path(dk, dv, dtype)
 
 
 def la_verify_chain(target, draft, tokens, count, uniform, accepted, next, B, T, V, dtype, stream):
@@ -646,20 +652,22 @@ def backward_saved(q, k, v, dout, saved, causal=True, eps=1e-6, workspace=None):
 # ---------------------------------------------------------------------------
 
 
-def _need_like(device, **tensors):
-    """Each value is (tensor, dtype, shape): contiguous, on ``device``, of that
-    dtype and shape (None tensors pass)."""
-    for name, (t, dtype, shape) in tensors.items():
+def _need_like(device, *tensors):
+    """Each of ``tensors`` is (name, tensor, dtype, shape): contiguous, on CUDA
+    device number ``device`` (-1: the host), of that dtype and shape; a tensor
+    that is None passes. One pass of cheap comparisons: these calls are often
+    shorter than their checks."""
+    for name, t, dtype, shape in tensors:
         if t is None:
             continue
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.get_device() != device:
+                raise ValueError(f"{name} must be on {'the host' if device < 0 else f'cuda:{device}'}, got {t.device}")
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _ptr(t):
@@ -671,17 +679,29 @@ def _shape4(t, name):
         raise ValueError(f"{name} must have 4 dimensions, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return tuple(t.shape)
+    return t.shape
+
+
+def _rows3(t, name):
+    if t.dim() != 3 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [B,T+1,V], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.shape[0], t.shape[1] - 1, t.shape[2]
 
 
 def _on(device, call, *args):
-    """call(*args, stream) with ``device`` current, on its current stream."""
+    """call(*args, stream) with CUDA device number ``device`` current, on its
+    current stream."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        _check(call(*args, torch.cuda.current_stream(device).cuda_stream))
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if torch.cuda.current_device() == device:
+        status = call(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(call(*args, torch.cuda.current_stream(device).cuda_stream))
+            status = call(*args, stream)
+    if status != LA_OK:
+        _check(status)
 
 
 def decode_tree(S, z, q, k, v, parent, alpha=None, eps=1e-6, count=None, out=None):
@@ -696,13 +716,13 @@ def decode_tree(S, z, q, k, v, parent, alpha=None, eps=1e-6, count=None, out=Non
     import torch
     B, H, dk, dv = _shape4(S, "S")
     T = _shape4(q, "q")[2]
-    dev, f32, i32 = S.device, torch.float32, torch.int32
+    dev, f32, i32 = S.get_device(), torch.float32, torch.int32
     code = _dtype_code(q)
     if out is None:
-        out = (torch.empty if count is None else torch.zeros)((B, H, T, dv), dtype=q.dtype, device=dev)
-    _need_like(dev, S=(S, f32, (B, H, dk, dv)), z=(z, f32, (B, H, dk)), q=(q, q.dtype, (B, H, T, dk)),
-               k=(k, q.dtype, (B, H, T, dk)), v=(v, q.dtype, (B, H, T, dv)), parent=(parent, i32, (B, T)),
-               alpha=(alpha, f32, (H,)), count=(count, i32, (B,)), out=(out, q.dtype, (B, H, T, dv)))
+        out = (torch.empty if count is None else torch.zeros)((B, H, T, dv), dtype=q.dtype, device=S.device)
+    _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("z", z, f32, (B, H, dk)), ("q", q, q.dtype, (B, H, T, dk)),
+               ("k", k, q.dtype, (B, H, T, dk)), ("v", v, q.dtype, (B, H, T, dv)), ("parent", parent, i32, (B, T)),
+               ("alpha", alpha, f32, (H,)), ("count", count, i32, (B,)), ("out", out, q.dtype, (B, H, T, dv)))
     _on(dev, la_decode_tree, S.data_ptr(), z.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
         parent.data_ptr(), _ptr(count), out.data_ptr(), B, H, T, dk, dv, _ptr(alpha), eps, code)
     return out
@@ -714,13 +734,13 @@ def decode_tree_delta(S, q, k, v, parent, count=None, out=None):
     import torch
     B, H, dk, dv = _shape4(S, "S")
     T = _shape4(q, "q")[2]
-    dev, f32, i32 = S.device, torch.float32, torch.int32
+    dev, f32, i32 = S.get_device(), torch.float32, torch.int32
     code = _dtype_code(q)
     if out is None:
-        out = (torch.empty if count is None else torch.zeros)((B, H, T, dv), dtype=q.dtype, device=dev)
-    _need_like(dev, S=(S, f32, (B, H, dk, dv)), q=(q, q.dtype, (B, H, T, dk)), k=(k, q.dtype, (B, H, T, dk)),
-               v=(v, q.dtype, (B, H, T, dv)), parent=(parent, i32, (B, T)), count=(count, i32, (B,)),
-               out=(out, q.dtype, (B, H, T, dv)))
+        out = (torch.empty if count is None else torch.zeros)((B, H, T, dv), dtype=q.dtype, device=S.device)
+    _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("q", q, q.dtype, (B, H, T, dk)), ("k", k, q.dtype, (B, H, T, dk)),
+               ("v", v, q.dtype, (B, H, T, dv)), ("parent", parent, i32, (B, T)), ("count", count, i32, (B,)),
+               ("out", out, q.dtype, (B, H, T, dv)))
     _on(dev, la_decode_tree_delta, S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), parent.data_ptr(),
         _ptr(count), out.data_ptr(), B, H, T, dk, dv, code)
     return out
@@ -731,15 +751,13 @@ def verify_chain(target, draft, tokens, uniform, count=None):
     target [B,T+1,V] and draft [B,T,V] probabilities (bf16 or f32), tokens [B,T]
     int32, uniform [B,T+1] f32 in [0, 1), count [B] int32 tokens of each."""
     import torch
-    if target.dim() != 3 or target.shape[1] < 1 or not target.is_cuda:
-        raise ValueError("target must be a CUDA tensor [B,T+1,V]")
-    B, T, V = target.shape[0], target.shape[1] - 1, target.shape[2]
-    dev, i32 = target.device, torch.int32
+    B, T, V = _rows3(target, "target")
+    dev, i32 = target.get_device(), torch.int32
     code = _dtype_code(target)
-    _need_like(dev, target=(target, target.dtype, (B, T + 1, V)), draft=(draft, target.dtype, (B, T, V)),
-               tokens=(tokens, i32, (B, T)), uniform=(uniform, torch.float32, (B, T + 1)), count=(count, i32, (B,)))
-    got = torch.empty((2, B), dtype=i32, device=dev)
-    accepted, nxt = got[0], got[1]
+    _need_like(dev, ("target", target, target.dtype, (B, T + 1, V)), ("draft", draft, target.dtype, (B, T, V)),
+               ("tokens", tokens, i32, (B, T)), ("uniform", uniform, torch.float32, (B, T + 1)), ("count", count, i32, (B,)))
+    got = torch.empty((2, B), dtype=i32, device=target.device)
+    accepted, nxt = got.unbind()
     _on(dev, la_verify_chain, target.data_ptr(), draft.data_ptr(), tokens.data_ptr(), _ptr(count),
         uniform.data_ptr(), accepted.data_ptr(), nxt.data_ptr(), B, T, V, code)
     return accepted, nxt
@@ -751,15 +769,13 @@ def verify_tree(target, tokens, parent, uniform, count=None):
     the committed state, row i + 1 after node i), tokens and parent [B,T] int32,
     uniform [B,T+1] f32 in [0, 1), count [B] int32 nodes of each."""
     import torch
-    if target.dim() != 3 or target.shape[1] < 1 or not target.is_cuda:
-        raise ValueError("target must be a CUDA tensor [B,T+1,V]")
-    B, T, V = target.shape[0], target.shape[1] - 1, target.shape[2]
-    dev, i32 = target.device, torch.int32
+    B, T, V = _rows3(target, "target")
+    dev, i32 = target.get_device(), torch.int32
     code = _dtype_code(target)
-    _need_like(dev, target=(target, target.dtype, (B, T + 1, V)), tokens=(tokens, i32, (B, T)),
-               parent=(parent, i32, (B, T)), uniform=(uniform, torch.float32, (B, T + 1)), count=(count, i32, (B,)))
-    got = torch.empty((B * (T + 2),), dtype=i32, device=dev)
-    path, accepted, nxt = got[2 * B:].view(B, T), got[:B], got[B:2 * B]
+    _need_like(dev, ("target", target, target.dtype, (B, T + 1, V)), ("tokens", tokens, i32, (B, T)),
+               ("parent", parent, i32, (B, T)), ("uniform", uniform, torch.float32, (B, T + 1)), ("count", count, i32, (B,)))
+    path = torch.empty((B, T), dtype=i32, device=target.device)
+    accepted, nxt = torch.empty((2, B), dtype=i32, device=target.device).unbind()
     _on(dev, la_verify_tree, target.data_ptr(), tokens.data_ptr(), parent.data_ptr(), _ptr(count),
         uniform.data_ptr(), path.data_ptr(), accepted.data_ptr(), nxt.data_ptr(), B, T, V, code)
     return path, accepted, nxt
@@ -774,15 +790,15 @@ def state_advance(S, z, k, v, path=None, accepted=None, alpha=None, S_out=None, 
     import torch
     B, H, dk, dv = _shape4(S, "S")
     T = _shape4(k, "k")[2]
-    dev, f32, i32 = S.device, torch.float32, torch.int32
+    dev, f32, i32 = S.get_device(), torch.float32, torch.int32
     code = _dtype_code(k)
     if (S_out is None) != (z_out is None):
         raise ValueError("S_out and z_out must be both given or both None")
     if S_out is None:
         S_out, z_out = S, z
-    _need_like(dev, S=(S, f32, (B, H, dk, dv)), z=(z, f32, (B, H, dk)), k=(k, k.dtype, (B, H, T, dk)),
-               v=(v, k.dtype, (B, H, T, dv)), path=(path, i32, (B, T)), accepted=(accepted, i32, (B,)),
-               alpha=(alpha, f32, (H,)), S_out=(S_out, f32, (B, H, dk, dv)), z_out=(z_out, f32, (B, H, dk)))
+    _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("z", z, f32, (B, H, dk)), ("k", k, k.dtype, (B, H, T, dk)),
+               ("v", v, k.dtype, (B, H, T, dv)), ("path", path, i32, (B, T)), ("accepted", accepted, i32, (B,)),
+               ("alpha", alpha, f32, (H,)), ("S_out", S_out, f32, (B, H, dk, dv)), ("z_out", z_out, f32, (B, H, dk)))
     _on(dev, la_state_advance, S.data_ptr(), z.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(path), _ptr(accepted),
         S_out.data_ptr(), z_out.data_ptr(), B, H, T, dk, dv, _ptr(alpha), code)
     return S_out, z_out
@@ -793,12 +809,12 @@ def state_advance_delta(S, k, v, path=None, accepted=None, S_out=None):
     import torch
     B, H, dk, dv = _shape4(S, "S")
     T = _shape4(k, "k")[2]
-    dev, f32, i32 = S.device, torch.float32, torch.int32
+    dev, f32, i32 = S.get_device(), torch.float32, torch.int32
     code = _dtype_code(k)
     if S_out is None:
         S_out = S
-    _need_like(dev, S=(S, f32, (B, H, dk, dv)), k=(k, k.dtype, (B, H, T, dk)), v=(v, k.dtype, (B, H, T, dv)),
-               path=(path, i32, (B, T)), accepted=(accepted, i32, (B,)), S_out=(S_out, f32, (B, H, dk, dv)))
+    _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("k", k, k.dtype, (B, H, T, dk)), ("v", v, k.dtype, (B, H, T, dv)),
+               ("path", path, i32, (B, T)), ("accepted", accepted, i32, (B,)), ("S_out", S_out, f32, (B, H, dk, dv)))
     _on(dev, la_state_advance_delta, S.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(path), _ptr(accepted),
         S_out.data_ptr(), B, H, T, dk, dv, code)
     return S_out
@@ -820,9 +836,9 @@ def _pool_args(S, z, codes, scales, z_pool, slot):
     f32, u8 = torch.float32, torch.uint8
     if (z is None) != (z_pool is None):
         raise ValueError("z and z_pool must be both given or both None")
-    _need_like(S.device, S=(S, f32, (B, H, dk, dv)), z=(z, f32, (B, H, dk)), codes=(codes, u8, (slots, H, dk, dv)),
-               scales=(scales, u8, (slots, H, dk, dv // min(32, dv) if dv else 0)), z_pool=(z_pool, f32, (slots, H, dk)),
-               slot=(slot, torch.int32, (B,)))
+    _need_like(S.get_device(), ("S", S, f32, (B, H, dk, dv)), ("z", z, f32, (B, H, dk)), ("codes", codes, u8, (slots, H, dk, dv)),
+               ("scales", scales, u8, (slots, H, dk, dv // min(32, dv) if dv else 0)), ("z_pool", z_pool, f32, (slots, H, dk)),
+               ("slot", slot, torch.int32, (B,)))
     return B, H, dk, dv, slots
 
 
@@ -831,7 +847,7 @@ def state_pack(S, codes, scales, slot, z=None, z_pool=None):
     int32 of a pool (state_pool): 8-bit codes with a power-of-two scale per
     block of min(32, dv) values (la_state_pack)."""
     B, H, dk, dv, slots = _pool_args(S, z, codes, scales, z_pool, slot)
-    _on(S.device, la_state_pack, S.data_ptr(), _ptr(z), codes.data_ptr(), scales.data_ptr(), _ptr(z_pool),
+    _on(S.get_device(), la_state_pack, S.data_ptr(), _ptr(z), codes.data_ptr(), scales.data_ptr(), _ptr(z_pool),
         slot.data_ptr(), B, H, dk, dv, slots)
 
 
@@ -839,6 +855,6 @@ def state_unpack(codes, scales, slot, S, z_pool=None, z=None):
     """The states of slots ``slot`` [B] int32 back into S [B,H,dk,dv] (and z)
     (la_state_unpack); sequences whose slot is outside the pool keep theirs."""
     B, H, dk, dv, slots = _pool_args(S, z, codes, scales, z_pool, slot)
-    _on(S.device, la_state_unpack, codes.data_ptr(), scales.data_ptr(), _ptr(z_pool), slot.data_ptr(),
+    _on(S.get_device(), la_state_unpack, codes.data_ptr(), scales.data_ptr(), _ptr(z_pool), slot.data_ptr(),
         S.data_ptr(), _ptr(z), B, H, dk, dv, slots)
     return S

@@ -45,7 +45,16 @@ struct PackArgs {
   cudaStream_t stream;
 };
 
+// Tree decode: on the CUDA cores (any head sizes and types), and on the tensor
+// cores where tree_on_tensor_cores says so.
 cudaError_t simt_tree(const TreeArgs& a);
+cudaError_t tree_mma_64_64(const TreeArgs& a);
+cudaError_t tree_mma_64_128(const TreeArgs& a);
+cudaError_t tree_mma_128_64(const TreeArgs& a);
+cudaError_t tree_mma_128_128(const TreeArgs& a);
+inline bool tree_on_tensor_cores(int dk, int dv, la_dtype dtype) {
+  return dtype == LA_BF16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128);
+}
 cudaError_t state_advance(const AdvanceArgs& a);
 cudaError_t verify(const VerifyArgs& a);
 cudaError_t state_pack(const PackArgs& a);

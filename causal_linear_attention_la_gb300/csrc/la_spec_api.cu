@@ -55,7 +55,13 @@ la_status tree_call(const char* who, const TreeArgs& a, int B, bool delta) {
     return fail(LA_ERR_INVALID_ARG, "%s: parent, count, alpha must be 4-byte aligned", who);
   TreeArgs t = a;
   t.BH = B * a.H;
-  const cudaError_t e = simt_tree(t);
+  cudaError_t e;
+  if (current_path() != LA_PATH_AUTO || !tree_on_tensor_cores(t.dk, t.dv, t.dtype))
+    e = simt_tree(t);
+  else if (t.dk == 64)
+    e = t.dv == 64 ? tree_mma_64_64(t) : tree_mma_64_128(t);
+  else
+    e = t.dv == 64 ? tree_mma_128_64(t) : tree_mma_128_128(t);
   return e == cudaSuccess ? LA_OK : cuda_fail(e, who);
 }
 
@@ -117,6 +123,11 @@ la_status pack_call(const char* who, const PackArgs& a, bool pack) {
 using namespace la;
 
 extern "C" {
+
+int la_tree_path(int dk, int dv, la_dtype dtype) {
+  if (!head_ok(dk) || !head_ok(dv) || (dtype != LA_F32 && dtype != LA_BF16)) return -1;
+  return current_path() == LA_PATH_AUTO && tree_on_tensor_cores(dk, dv, dtype) ? 1 : 0;
+}
 
 la_status la_decode_tree(const float* S, const float* z, const void* q, const void* k, const void* v,
                          const int* parent, const int* count, void* out, int B, int H, int T, int dk, int dv,

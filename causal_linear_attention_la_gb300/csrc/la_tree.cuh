@@ -1,6 +1,8 @@
 // Shared by the tree-decode kernels: the path of every node of a drafted tree.
 #pragma once
 
+#include <atomic>
+
 #include "la_spec.cuh"
 
 namespace la {
@@ -13,12 +15,48 @@ __device__ __forceinline__ int tree_parent(const int* parent, int i) {
   return p >= 0 && p < i ? p : -1;
 }
 
-// The nodes on node i's path, i among them, as a bit mask. `par` holds the
-// sanitised parents.
-__device__ __forceinline__ unsigned long long tree_path_mask(const int* par, int i) {
-  unsigned long long m = 0ull;
-  for (int p = i; p >= 0; p = par[p]) m |= 1ull << p;
-  return m;
+// The nodes on each node's path, the node among them, as bit masks, and the
+// path's length: one warp, lane l for nodes l and l + 32, by pointer doubling
+// (after r rounds a mask holds the nearest 2^r nodes and `up` points past
+// them), six rounds for the longest path. Entries n .. n_pad-1 are zero.
+// `up` is scratch of kTreeMax ints.
+__device__ __forceinline__ void tree_masks(const int* parent, int n, int n_pad, unsigned long long* mask, int* depth,
+                                           int* up) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long m[2];
+  int u[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 32 * h;
+    m[h] = i < n ? 1ull << i : 0ull;
+    u[h] = i < n ? tree_parent(parent, i) : -1;
+  }
+  while (__any_sync(0xffffffffu, u[0] >= 0 || u[1] >= 0)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h;
+      if (i < n) {
+        mask[i] = m[h];
+        up[i] = u[h];
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (u[h] >= 0) {
+        m[h] |= mask[u[h]];
+        u[h] = up[u[h]];
+      }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 32 * h;
+    if (i < n_pad) {
+      mask[i] = m[h];
+      depth[i] = __popcll(m[h]);
+    }
+  }
 }
 
 // a^n for 0 <= n <= kTreeMax by squaring: at most 12 roundings, and exact for
@@ -33,5 +71,22 @@ __device__ __forceinline__ float tree_power(float a, int n) {
 __device__ __forceinline__ int clamp_count(const int* count, int b, int T) {
   return count == nullptr ? T : min(max(count[b], 0), T);
 }
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device,
+// asked for once per kernel and device.
+struct SharedMemoryOnce {
+  std::atomic<unsigned long long> done{0ull};
+  template <typename Kernel>
+  cudaError_t allow(Kernel kern, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 }  // namespace la

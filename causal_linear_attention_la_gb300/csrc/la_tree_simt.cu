@@ -38,7 +38,7 @@ struct TreeShape {
 // Shared-memory layout in floats for T nodes.
 template <int DK, int DV, bool kDelta>
 struct TreeSmem {
-  int TP, WP, q, k, v, w, w2, qs, part, z, den, pw, depth, mask, par, total;
+  int TP, WP, q, k, v, w, w2, qs, part, z, den, pw, depth, mask, up, total;
   __host__ __device__ explicit TreeSmem(int T) {
     using Sh = TreeShape<DK, DV>;
     TP = (T + 3) & ~3;
@@ -54,8 +54,8 @@ struct TreeSmem {
     den = z + DK;
     pw = den + TP;
     depth = pw + kTreeMax + 4;
-    par = depth + TP;
-    mask = par + TP;                 // 8-byte entries
+    up = depth + TP;
+    mask = up + TP;                 // 8-byte entries
     mask = (mask + 1) & ~1;
     total = mask + 2 * TP;
   }
@@ -140,7 +140,7 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   float* part = sm + L.part;
   float* pw = sm + L.pw;
   int* depth = reinterpret_cast<int*>(sm + L.depth);
-  int* par = reinterpret_cast<int*>(sm + L.par);
+  int* up = reinterpret_cast<int*>(sm + L.up);
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(sm + L.mask);
 
   // the state: thread (rg, cg) holds rows rg*E .. rg*E+E-1, columns 4cg .. 4cg+3
@@ -168,17 +168,11 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
     fk[i * QP + r] = c;
   }
   for (int x = tid; x < TP * DV; x += NT) vs[x] = x / DV < n ? to_f32<T>(vb[x]) : 0.f;
-  for (int i = tid; i < TP; i += NT) par[i] = i < n ? tree_parent(parent + (long long)b * ntok, i) : -1;
+  if (tid < 32) tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, up);
   if (!kDelta) {
     for (int r = tid; r < DK; r += NT) sm[L.z + r] = z[bh * DK + r];
     const float a = alpha != nullptr ? alpha[h] : 1.f;
     for (int i = tid; i <= kTreeMax; i += NT) pw[i] = tree_power(a, i);
-  }
-  __syncthreads();
-  for (int i = tid; i < TP; i += NT) {
-    const unsigned long long m = i < n ? tree_path_mask(par, i) : 0ull;
-    mask[i] = m;
-    depth[i] = __popcll(m);
   }
   __syncthreads();
 
@@ -298,7 +292,8 @@ template <int DK, int DV, typename T, bool kDelta>
 cudaError_t launch(const TreeArgs& a) {
   const int smem = TreeSmem<DK, DV, kDelta>(a.T).total * (int)sizeof(float);
   auto kern = tree_simt_kernel<DK, DV, T, kDelta>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SharedMemoryOnce once;
+  cudaError_t e = once.allow(kern, TreeSmem<DK, DV, kDelta>(kTreeMax).total * (int)sizeof(float));
   if (e != cudaSuccess) return e;
   kern<<<a.BH, TreeShape<DK, DV>::NT, smem, a.stream>>>(a.S, a.z, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.parent,
                                                         a.count, (T*)a.out, a.H, a.T, a.alpha, a.eps);

@@ -360,11 +360,18 @@ LA_API la_status la_state_copy(float* dst_S, float* dst_z, const float* src_S,
  *        0 .. T); the rows behind them are neither read nor written. NULL: T.
  * T <= LA_TREE_MAX (LA_ERR_UNSUPPORTED above); T = 0 is a no-op.
  * A node off a path never reaches its outputs, whatever its rows hold
- * (infinities and NaN included). fp32 arithmetic.
+ * (infinities and NaN included). fp32 arithmetic; where la_tree_path is 1 the
+ * products run on the tensor cores, fp32 operands as bf16 high and low parts
+ * (below 2^-16 of the sum of the terms' magnitudes), summed in fp32.
  */
 LA_API la_status la_decode_tree(const float* S, const float* z, const void* q, const void* k, const void* v,
                                 const int* parent, const int* count, void* out, int B, int H, int T, int dk,
                                 int dv, const float* alpha, float eps, la_dtype dtype, la_stream_t stream);
+
+/* Which kernel la_decode_tree and la_decode_tree_delta take under the current
+ * la_set_path setting: 1 = tensor-core (bf16, dk and dv in {64, 128}),
+ * 0 = CUDA-core; -1 if unsupported. */
+LA_API int la_tree_path(int dk, int dv, la_dtype dtype);
 
 /*
  * Tree decode by the delta rule: every node's output as if

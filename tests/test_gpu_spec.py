@@ -37,8 +37,15 @@ def _lib():
     assert la.la_device_status(True) == la.LA_OK
 
 
-def gamma(dk, depth=1):
-    return 2 * (dk + 64 + 32) * 2.0 ** -24 * depth
+def gamma(dk, depth=1, tc=False):
+    """On the tensor cores every term is off by 2^-16 of itself on top (fp32
+    operands as two bf16 parts): in the pair products and again where they
+    weight a value, numerator and denominator, so four times."""
+    return (2 * (dk + 64 + 32) * 2.0 ** -24 + (4 * 2.0 ** -16 if tc else 0.0)) * depth
+
+
+def on_tc(dk, dv, dtype):
+    return la.la_tree_path(dk, dv, la.LA_BF16 if dtype == "bf16" else la.LA_F32) == 1
 
 
 def near(got, want, scale, dtype, g):
@@ -86,7 +93,7 @@ def tree(B, T, seed, lean=0.5):
 
 TREES = [(1, 1, 1, 16, 16), (2, 3, 2, 32, 64), (1, 2, 7, 64, 64), (2, 2, 8, 128, 128), (2, 1, 9, 128, 32), (1, 2, 16, 64, 128),
          (2, 2, 31, 128, 128), (1, 1, 32, 16, 128), (1, 3, 33, 32, 32), (2, 2, 63, 64, 64), (2, 3, 64, 128, 128),
-         (1, 1, 64, 128, 16), (3, 2, 17, 16, 64)]
+         (1, 1, 64, 128, 16), (3, 2, 17, 16, 64), (2, 2, 3, 64, 128), (1, 2, 40, 128, 64), (2, 1, 49, 64, 128), (1, 3, 11, 128, 64)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -108,8 +115,33 @@ def test_tree(B, H, T, dk, dv, rule, dtype):
         out = la.decode_tree(Sd, cuda(z), *args, alpha=None if alpha is None else cuda(alpha))
         want, scale = spec.decode_tree(S, z, q, k, v, parent, alpha)
     assert out.dtype == args[0].dtype
-    near(to_host(out), want, scale, dtype, gamma(dk, T if delta else 1))
+    near(to_host(out), want, scale, dtype, gamma(dk, T if delta else 1, on_tc(dk, dv, dtype)))
     assert torch.equal(Sd.cpu(), torch.from_numpy(S)), "the state is only read"
+
+
+@pytest.mark.parametrize("rule", ["plain", "decay", "delta"])
+@pytest.mark.parametrize("T", [1, 5, 16, 24, 47, 64])
+def test_tree_on_cuda_cores_agrees(T, rule):
+    """The CUDA-core kernel on bf16 rows of the tensor-core shapes."""
+    B, H, d = 2, 2, 64
+    delta = rule == "delta"
+    S, z = state(B, H, d, d, T, delta)
+    q, k, v = rows(B, H, T, d, d, T + 1, "bf16", delta)
+    parent = tree(B, T, T + 2)
+    alpha = np.linspace(0.6, 1.0, H).astype(np.float32) if rule == "decay" else None
+    args = [to_dev(x, "bf16") for x in (q, k, v)] + [i32(parent)]
+    prev = la.la_set_path(la.LA_PATH_SIMT)
+    try:
+        assert la.la_tree_path(d, d, la.LA_BF16) == 0
+        if delta:
+            out = la.decode_tree_delta(cuda(S), *args)
+            want, scale = spec.decode_tree_delta(S, q, k, v, parent)
+        else:
+            out = la.decode_tree(cuda(S), cuda(z), *args, alpha=None if alpha is None else cuda(alpha))
+            want, scale = spec.decode_tree(S, z, q, k, v, parent, alpha)
+        near(to_host(out), want, scale, "bf16", gamma(d, T if delta else 1))
+    finally:
+        la.la_set_path(prev)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -137,7 +169,7 @@ def test_tree_ragged(delta, dtype):
     for b, n in enumerate(count):
         n = min(max(n, 0), T)
         assert np.all(got[b, :, n:] == 7.0)
-        near(got[b, :, :n], want[b, :, :n], scale[b, :, :n], dtype, gamma(d, T if delta else 1))
+        near(got[b, :, :n], want[b, :, :n], scale[b, :, :n], dtype, gamma(d, T if delta else 1, on_tc(d, d, dtype)))
     # out allocated by the call: zeros behind the last node
     if not delta:
         got = to_host(la.decode_tree(cuda(S), cuda(z), *args, count=i32(count)))
@@ -172,13 +204,13 @@ def test_tree_nonfinite_rows_off_the_path(delta, d, dtype):
             args = [to_dev(y, dtype) for y in (q, k2, v2)] + [i32(parent)]
             out = la.decode_tree_delta(cuda(S), *args) if delta else la.decode_tree(cuda(S), cuda(z), *args)
             got = to_host(out)
-            near(got[:, :, clean], want[:, :, clean], scale[:, :, clean], dtype, gamma(d, T if delta else 1))
+            near(got[:, :, clean], want[:, :, clean], scale[:, :, clean], dtype, gamma(d, T if delta else 1, on_tc(d, d, dtype)))
             if kv == "v" and np.isnan(x):
                 assert np.all(np.isnan(got[:, :, soiled][..., ::3]))
                 if not delta:
                     cols = np.ones(d, bool)
                     cols[::3] = False
-                    near(got[..., cols], want[..., cols], scale[..., cols], dtype, gamma(d))
+                    near(got[..., cols], want[..., cols], scale[..., cols], dtype, gamma(d, 1, on_tc(d, d, dtype)))
 
 
 def test_tree_parents_out_of_range():
@@ -206,7 +238,7 @@ def test_tree_decay_extremes(alpha):
         a = np.full(H, alpha, np.float32)
         got = to_host(la.decode_tree(cuda(S), cuda(z), *[to_dev(x, dtype) for x in (q, k, v)], i32(parent), alpha=cuda(a)))
         want, scale = spec.decode_tree(S, z, q, k, v, parent, a)
-        near(got, want, scale, dtype, gamma(d))
+        near(got, want, scale, dtype, gamma(d, 1, on_tc(d, d, dtype)))
 
 
 def test_tree_of_one_path_matches_decode_steps():
@@ -497,7 +529,7 @@ def test_state_offsets_past_32_bits():
         t[-1] = to_dev(x[0], "bf16")
     out = la.decode_tree(S, z, *big, torch.full((B, 1), -1, dtype=torch.int32, device="cuda"))
     want, scale = spec.decode_tree(S1, z1, q, k, v, [[-1]])
-    near(to_host(out[-1:]), want, scale, "bf16", gamma(d))
+    near(to_host(out[-1:]), want, scale, "bf16", gamma(d, 1, True))
     codes, scales, _ = la.state_pool(B, H, d, d)
     slot = torch.arange(B, dtype=torch.int32, device="cuda")
     la.state_pack(S, codes, scales, slot)
@@ -554,7 +586,7 @@ def test_a_turn():
     assert np.array_equal(path.cpu().numpy(), wp) and np.array_equal(accepted.cpu().numpy(), wa)
     assert np.array_equal(nxt.cpu().numpy(), wn)
     want, scale = spec.decode_tree(S, z, q, k, v, parent, alpha)
-    near(to_host(out), want, scale, "bf16", gamma(128))
+    near(to_host(out), want, scale, "bf16", gamma(128, 1, True))
     wS, wz, A = spec.advance(S, z, k, v, wp, wa, alpha)
     near(to_host(dev[0]), wS, A, "f32", 64 * 2.0 ** -24)
     near(to_host(dev[1]), wz, wz, "f32", 64 * 2.0 ** -24)
@@ -564,7 +596,7 @@ def test_a_turn():
         if n:
             at = wp[b, :n]
             S2, z2, steps = orc.decode_steps_decay(S[b], z[b], q[b][:, at], k[b][:, at], v[b][:, at], alpha=alpha)
-            near(to_host(out)[b][:, at], steps, scale[b][:, at], "bf16", gamma(128))
+            near(to_host(out)[b][:, at], steps, scale[b][:, at], "bf16", gamma(128, 1, True))
     # and the snapshot brings the first state back, to its 8 bits
     back, zb = dev[0].clone(), dev[1].clone()
     la.state_unpack(dev[9], dev[10], dev[12], back, z_pool=dev[11], z=zb)

@@ -2,7 +2,6 @@
 before any device work, empty problems are accepted, and the Python layer
 checks what it is given."""
 
-import numpy as np
 import pytest
 import torch
 
@@ -47,6 +46,17 @@ def test_tree_delta_refusals():
     assert f(q=1028) == INVALID and f(parent=3) == INVALID
     assert f(T=65) == UNSUPPORTED and f(dk=24) == UNSUPPORTED
     assert f(B=0) == OK and f(T=0) == OK
+
+
+def test_tree_path():
+    assert la.la_tree_path(128, 128, la.LA_BF16) == 1 and la.la_tree_path(64, 128, la.LA_BF16) == 1
+    assert la.la_tree_path(128, 128, la.LA_F32) == 0 and la.la_tree_path(32, 64, la.LA_BF16) == 0
+    assert la.la_tree_path(48, 64, la.LA_BF16) == -1 and la.la_tree_path(64, 64, 7) == -1
+    prev = la.la_set_path(la.LA_PATH_SIMT)
+    try:
+        assert la.la_tree_path(128, 128, la.LA_BF16) == 0
+    finally:
+        la.la_set_path(prev)
 
 
 def test_verify_refusals(lib):
@@ -139,15 +149,13 @@ def test_python_layer_checks():
 
 def test_python_shape_checks():
     """The checks that stand between a wrong shape and the kernels."""
-    cpu = torch.device("cpu")
     t = torch.zeros(2, 3)
-    la._need_like(cpu, a=(t, torch.float32, (2, 3)), b=(None, torch.int32, (9,)))
-    with pytest.raises(ValueError, match="shape"):
-        la._need_like(cpu, a=(t, torch.float32, (3, 2)))
+    la._need_like(-1, ("a", t, torch.float32, (2, 3)), ("b", None, torch.int32, (9,)))
+    with pytest.raises(ValueError, match="a must have shape"):
+        la._need_like(-1, ("a", t, torch.float32, (3, 2)))
     with pytest.raises(TypeError, match="float64"):
-        la._need_like(cpu, a=(t, torch.float64, (2, 3)))
+        la._need_like(-1, ("a", t, torch.float64, (2, 3)))
     with pytest.raises(ValueError, match="contiguous"):
-        la._need_like(cpu, a=(t.t(), torch.float32, (3, 2)))
-    with pytest.raises(ValueError, match="on cuda"):
-        la._need_like(torch.device("cuda", 0), a=(t, torch.float32, (2, 3)))
-    assert np.isfinite(la.LA_TREE_MAX)
+        la._need_like(-1, ("a", t.t(), torch.float32, (3, 2)))
+    with pytest.raises(ValueError, match="on cuda:0"):
+        la._need_like(0, ("a", t, torch.float32, (2, 3)))
