@@ -59,9 +59,9 @@ struct Shape {
 // Byte offsets in shared memory for up to `TP` nodes (a multiple of 16).
 template <int DK, int DV, int NTM, bool kDelta>
 struct Layout {
-  int qh, ql, kh, kl, v, vl, wh, wl, r, a, mask, depth, up, pw, den, bad, total;
+  int qh, ql, kh, kl, v, vl, wh, wl, r, a, mask, depth, up, pw, zq, den, bad, total;
   __host__ __device__ constexpr explicit Layout(int TP)
-      : qh(0), ql(0), kh(0), kl(0), v(0), vl(0), wh(0), wl(0), r(0), a(0), mask(0), depth(0), up(0), pw(0), den(0), bad(0),
+      : qh(0), ql(0), kh(0), kl(0), v(0), vl(0), wh(0), wl(0), r(0), a(0), mask(0), depth(0), up(0), pw(0), zq(0), den(0), bad(0),
         total(0) {
     using Sh = Shape<DK, DV, NTM, kDelta>;
     int at = 0;
@@ -100,8 +100,10 @@ struct Layout {
     at += TP * 4;
     pw = at;
     at += (kTreeMax + 4) * 4;
-    den = at;
+    zq = at;
     at += TP * 4;
+    den = at;
+    at += NTM * TP * 4;
     total = at;
   }
 };
@@ -159,12 +161,16 @@ __device__ __forceinline__ void store_columns(uint8_t* row, int chunk, const uin
   *reinterpret_cast<uint2*>(p + 16) = odd;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 template <int DK, int DV, int NTM, bool kDelta>
 __global__ void __launch_bounds__(2 * DV, 512 / (2 * DV))
 tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const __nv_bfloat16* __restrict__ q,
                 const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                 const int* __restrict__ parent, const int* __restrict__ count, __nv_bfloat16* __restrict__ out, int H,
-                int ntok, const float* __restrict__ alpha, float eps) {
+                int ntok, const float* __restrict__ alpha, float eps, int ahead) {
   using Sh = Shape<DK, DV, NTM, kDelta>;
   constexpr int NT = Sh::NT, NW = Sh::NW, KS = Sh::KS, QP = Sh::QP, VP = Sh::VP, WP = Sh::WP, RP = Sh::RP, AP = Sh::AP;
   extern __shared__ __align__(16) uint8_t sm[];
@@ -178,7 +184,8 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
   unsigned int* bad = reinterpret_cast<unsigned int*>(sm + L.bad);
   int* depth = reinterpret_cast<int*>(sm + L.depth);
   float* pw = reinterpret_cast<float*>(sm + L.pw);
-  float* den = reinterpret_cast<float*>(sm + L.den);
+  float* zqs = reinterpret_cast<float*>(sm + L.zq);      // phi(q_i) . z
+  float* den = reinterpret_cast<float*>(sm + L.den);     // [tile of j][i]: sums of W over a tile
   float* R = reinterpret_cast<float*>(sm + L.r);
   float* A = reinterpret_cast<float*>(sm + L.a);
 
@@ -216,13 +223,16 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[ks][e] = *reinterpret_cast<const float2*>(Sb + (16 * ks + e) * DV);
   }
-  if (tid == 0) bad[0] = bad[1] = 0u;
-  if (warp == 0)
-    tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, reinterpret_cast<int*>(sm + L.up));
-  if (!kDelta) {
-    const float a = alpha != nullptr ? alpha[h] : 1.f;
+  // the state and rows of the CTA that follows in this one's place, into L2
+  if (tid == NT - 1 && bh + ahead < gridDim.x) {
+    prefetch_l2(S + (bh + ahead) * (long long)(DK * DV), DK * DV * 4);
+    prefetch_l2(q + (bh + ahead) * (long long)ntok * DK, ntok * DK * 2);
+    prefetch_l2(k + (bh + ahead) * (long long)ntok * DK, ntok * DK * 2);
+    prefetch_l2(v + (bh + ahead) * (long long)ntok * DV, ntok * DV * 2);
+  }
+  if (!kDelta && alpha != nullptr) {
+    const float a = alpha[h];
     for (int d = tid; d <= kTreeMax; d += NT) pw[d] = tree_power(a, d);
-    __syncthreads();                               // `bad` is clear before v is looked at
   }
 
   // ---- rows
@@ -258,7 +268,7 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
       // phi(q_i) . z over the CH lanes of the row
 #pragma unroll
       for (int o = 1; o < CH; o <<= 1) zq += __shfl_xor_sync(0xffffffffu, zq, o);
-      if (ch == 0 && i < TP) den[i] = zq;
+      if (ch == 0 && i < TP) zqs[i] = zq;
     }
     i += RPP;
     if (i >= TP) break;
@@ -268,17 +278,16 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
       xk = *reinterpret_cast<const uint4*>(kb + i * DK + 8 * ch);
     }
   }
+  int odd_values = 0;
   if (!kDelta) {
     for (;;) {
       if (iv < TP) {
         uint32_t* p = reinterpret_cast<uint32_t*>(&xv);
-        bool any = false;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          if (nonfinite_half(p[w])) { p[w] &= 0xffff0000u; any = true; }
-          if (nonfinite_half(p[w] >> 16)) { p[w] &= 0x0000ffffu; any = true; }
+          if (nonfinite_half(p[w])) { p[w] &= 0xffff0000u; odd_values = 1; }
+          if (nonfinite_half(p[w] >> 16)) { p[w] &= 0x0000ffffu; odd_values = 1; }
         }
-        if (any) atomicOr(bad + (iv >> 5), 1u << (iv & 31));
         store_columns(sm + L.v + iv * VP, chv, xv);
       }
       iv += RPV;
@@ -286,7 +295,20 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
       xv = iv < n ? *reinterpret_cast<const uint4*>(vb + iv * DV + 8 * chv) : zero4;
     }
   }
-  __syncthreads();
+  if (warp == NW - 1)
+    tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, reinterpret_cast<int*>(sm + L.up));
+  unsigned long long spoilt = 0ull;                // nodes with values that v's operand leaves out
+  if (kDelta) {
+    if (tid == 0) bad[0] = bad[1] = 0u;
+    __syncthreads();
+  } else if (__syncthreads_or(odd_values)) {
+    if (tid == 0) bad[0] = bad[1] = 0u;
+    __syncthreads();
+    for (int x = tid; x < n * DV; x += NT)
+      if (nonfinite(__bfloat162float(vb[x]))) atomicOr(bad + ((x / DV) >> 5), 1u << ((x / DV) & 31));
+    __syncthreads();
+    spoilt = (unsigned long long)bad[0] | ((unsigned long long)bad[1] << 32);
+  }
 
   // ---- pairs: tiles of 16 nodes i x 8 nodes j, j <= i's tile
   {
@@ -342,6 +364,12 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
           split2(w0, w1, hi, lo);
           *reinterpret_cast<uint32_t*>(sm + L.wh + row * WP + 2 * col) = hi;
           *reinterpret_cast<uint32_t*>(sm + L.wl + row * WP + 2 * col) = lo;
+          if constexpr (!kDelta) {
+            float x = w0 + w1;                     // over the row's four lanes
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            if (t == 0) den[nj * TP + row] = x;
+          }
         }
       }
     // the j of a last half step that no tile covers
@@ -457,18 +485,6 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
     }
     __syncthreads();
   } else {
-    // ---- den_i = a^d_i phi(q_i).z + sum_j W[i][j] + eps, a warp per node
-    for (int r = warp; r < n; r += NW) {
-      float x = 0.f;
-      for (int j = 2 * lane; j <= r; j += 64) {
-        const uint32_t hi = *reinterpret_cast<const uint32_t*>(sm + L.wh + r * WP + 2 * j);
-        const uint32_t lo = *reinterpret_cast<const uint32_t*>(sm + L.wl + r * WP + 2 * j);
-        x += (low_half(hi) + low_half(lo)) + (high_half(hi) + high_half(lo));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (lane == 0) den[r] = 1.f / (fmaf(pw[depth[r]], den[r], x) + eps);
-    }
     // the read's part of a node decays along its whole path
     if (alpha != nullptr) {
 #pragma unroll
@@ -508,10 +524,8 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
           }
       }
   }
-  if (!kDelta) __syncthreads();                    // den
-
   // ---- out: lane holds nodes 8 nt + 2t (+ 1), columns c0, c0 + 1
-  const unsigned long long spoilt = (unsigned long long)bad[0] | ((unsigned long long)bad[1] << 32);
+  if constexpr (kDelta) spoilt = (unsigned long long)bad[0] | ((unsigned long long)bad[1] << 32);
 #pragma unroll
   for (int nt = 0; nt < NTM; ++nt)
     if (nt < tiles) {
@@ -538,9 +552,15 @@ tree_mma_kernel(const float* __restrict__ S, const float* __restrict__ z, const 
             if (nonfinite(x1)) o1 = fmaf(w, x1, o1);
           }
         }
-        if (!kDelta) {
-          o0 *= den[node];
-          o1 *= den[node];
+        if constexpr (!kDelta) {
+          // den_i = a^d_i phi(q_i).z + sum_j W[i][j] + eps
+          float x = zqs[node];
+          if (alpha != nullptr) x *= pw[depth[node]];
+#pragma unroll
+          for (int nj = 0; nj <= nt; ++nj) x += den[nj * TP + node];
+          const float r = 1.f / (x + eps);
+          o0 *= r;
+          o1 *= r;
         }
         *reinterpret_cast<uint32_t*>(ob + (long long)node * DV + c0) = pack2(o0, o1);
       }
@@ -556,9 +576,14 @@ cudaError_t launch(const TreeArgs& a) {
   static SharedMemoryOnce once;
   cudaError_t e = once.allow(kern, most.total);
   if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0, resident = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, 2 * DV, L.total);
+  if (e != cudaSuccess) return e;
   kern<<<a.BH, 2 * DV, L.total, a.stream>>>(a.S, a.z, (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.k,
                                             (const __nv_bfloat16*)a.v, a.parent, a.count, (__nv_bfloat16*)a.out, a.H, a.T,
-                                            a.alpha, a.eps);
+                                            a.alpha, a.eps, sms * resident);
   e = cudaGetLastError();
   if (e == cudaSuccess) note_launch();
   return e;
