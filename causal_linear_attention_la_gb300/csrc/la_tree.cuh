@@ -72,20 +72,27 @@ __device__ __forceinline__ int clamp_count(const int* count, int b, int T) {
   return count == nullptr ? T : min(max(count[b], 0), T);
 }
 
-// Lets a kernel use `bytes` of dynamic shared memory on the current device,
-// asked for once per kernel and device.
-struct SharedMemoryOnce {
-  std::atomic<unsigned long long> done{0ull};
+// Lets a kernel use `bytes` of dynamic shared memory and counts the CTAs of it
+// that the current device holds at once, asked for once per device.
+struct KernelOnce {
+  static constexpr int kDevices = 64;
+  std::atomic<int> held[kDevices] = {};
   template <typename Kernel>
-  cudaError_t allow(Kernel kern, int bytes) {
+  cudaError_t prepare(Kernel kern, int threads, int bytes, int* resident) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const bool keep = dev >= 0 && dev < kDevices;
+    *resident = keep ? held[dev].load(std::memory_order_relaxed) : 0;
+    if (*resident > 0) return cudaSuccess;
+    int sms = 0, per = 0;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, bytes);
+    if (e != cudaSuccess) return e;
+    *resident = sms * (per > 0 ? per : 1);
+    if (keep) held[dev].store(*resident, std::memory_order_relaxed);
+    return cudaSuccess;
   }
 };
 

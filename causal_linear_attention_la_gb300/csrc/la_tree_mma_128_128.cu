@@ -1,6 +1,11 @@
 // Tree decode on the tensor cores, dk = 128, dv = 128.
-#include "la_tree_mma.cuh"
+#include "la_tree_small.cuh"
+#include "la_tree_wide.cuh"
 
 namespace la {
-cudaError_t tree_mma_128_128(const TreeArgs& a) { return treemma::dispatch<128, 128>(a); }
+cudaError_t tree_mma_128_128(const TreeArgs& a) {
+  if (a.T <= treesmall::TP)
+    return a.z == nullptr ? treesmall::launch<128, 128, true>(a) : treesmall::launch<128, 128, false>(a);
+  return a.z == nullptr ? treewide::launch<128, 128, true>(a) : treewide::launch<128, 128, false>(a);
+}
 }  // namespace la

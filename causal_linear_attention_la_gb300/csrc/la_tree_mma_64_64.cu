@@ -1,6 +1,11 @@
 // Tree decode on the tensor cores, dk = 64, dv = 64.
-#include "la_tree_mma.cuh"
+#include "la_tree_small.cuh"
+#include "la_tree_wide.cuh"
 
 namespace la {
-cudaError_t tree_mma_64_64(const TreeArgs& a) { return treemma::dispatch<64, 64>(a); }
+cudaError_t tree_mma_64_64(const TreeArgs& a) {
+  if (a.T <= treesmall::TP)
+    return a.z == nullptr ? treesmall::launch<64, 64, true>(a) : treesmall::launch<64, 64, false>(a);
+  return a.z == nullptr ? treewide::launch<64, 64, true>(a) : treewide::launch<64, 64, false>(a);
+}
 }  // namespace la

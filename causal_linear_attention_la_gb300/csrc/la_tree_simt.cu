@@ -292,8 +292,10 @@ template <int DK, int DV, typename T, bool kDelta>
 cudaError_t launch(const TreeArgs& a) {
   const int smem = TreeSmem<DK, DV, kDelta>(a.T).total * (int)sizeof(float);
   auto kern = tree_simt_kernel<DK, DV, T, kDelta>;
-  static SharedMemoryOnce once;
-  cudaError_t e = once.allow(kern, TreeSmem<DK, DV, kDelta>(kTreeMax).total * (int)sizeof(float));
+  static KernelOnce once;
+  int resident = 0;
+  cudaError_t e = once.prepare(kern, TreeShape<DK, DV>::NT, TreeSmem<DK, DV, kDelta>(kTreeMax).total * (int)sizeof(float),
+                               &resident);
   if (e != cudaSuccess) return e;
   kern<<<a.BH, TreeShape<DK, DV>::NT, smem, a.stream>>>(a.S, a.z, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.parent,
                                                         a.count, (T*)a.out, a.H, a.T, a.alpha, a.eps);

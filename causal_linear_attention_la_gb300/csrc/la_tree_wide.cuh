@@ -1,0 +1,582 @@
+// Tree decode on the tensor cores for 17 to 64 nodes (the formulas of
+// la_tree_simt.cu, the operands and precision of la_tree_ops.cuh).
+//
+// With 64 nodes at d = 128 a head moves 128 KiB (5600 cycles of an SM's share
+// of HBM) and takes 2256 mma instructions, 4500 cycles of the SM's tensor pipe:
+// the two are level, and what costs is everything beside them. One CTA per
+// (batch, head), two per SM: one warp per 16 value columns and one more that
+// brings the state in and works out the ancestor masks.
+//   rows    phi(q), phi(k) as bf16 hi and lo, v, phi(q).z; the next pass's
+//           loads in flight while one is worked on
+//   pairs   16 x 16 tiles of node pairs on and below the diagonal, dealt to
+//           the warps; mask and decay applied, W stored as hi and lo, row sums
+//           per tile
+//   read    D = S^T x: the state comes by TMA in slabs of 32 rows (boxes of 32
+//           columns with the 128-byte swizzle, so that a fragment's rows lie
+//           in different banks) through two buffers; a slab is used for all
+//           nodes at once
+//   path    D += V^T W^T in steps of 16 nodes, out
+// Up to 48 nodes the slabs have buffers of their own and start with the CTA;
+// above, two CTAs per SM leave no room and the buffers are where phi(k) was,
+// from the pairs on. (The state straight from global memory into the lanes'
+// registers, as fragments of 64 bytes, cost twice the wavefronts and 64
+// registers a thread: 79 us on 1536 decay-gated states of up to 64 nodes.)
+//
+// The delta rule reads for keys and queries in one pass over the slabs (their
+// buffers become R = v - S^T k), solves for u with two lanes a column, in
+// blocks of 8 nodes, and u (hi and lo) takes the place of q and k.
+#pragma once
+
+#include "la_tree_ops.cuh"
+
+namespace la {
+namespace treewide {
+
+using namespace treeops;
+
+constexpr int SLAB = 32;                       // state rows per slab
+constexpr int TM = 64;                         // most nodes
+
+template <int DK, int DV, bool kDelta>
+struct Wide {
+  static constexpr int NT = 2 * DV, NW = DV / 16;
+  static constexpr int SLABS = DK / SLAB;
+  static constexpr int BUF = SLAB * DV * 4;              // bytes of a slab
+  static constexpr int QP = 2 * DK + 16, VP = 2 * DV + 16;
+  static constexpr int WP = 2 * TM + 16;
+  static constexpr int RP = DV + 16;                     // floats per row of R: the two lanes of a column in different banks
+  static constexpr int AP = TM + 4;
+  int ring, qh, ql, kh, kl, v, vl, wh, wl, r, a, mask, depth, up, pw, zq, den, rden, bad, bar, total;
+  bool overlay;                                          // the ring lies where phi(k) was
+  __host__ __device__ constexpr explicit Wide(int TP)
+      : ring(0), qh(0), ql(0), kh(0), kl(0), v(0), vl(0), wh(0), wl(0), r(0), a(0), mask(0), depth(0), up(0), pw(0), zq(0),
+        den(0), rden(0), bad(0), bar(0), total(0), overlay(false) {
+    int at = 0;
+    if (kDelta) {
+      ring = r = at;                                     // R after the last slab
+      at += TP * RP * 4 > 2 * BUF ? TP * RP * 4 : 2 * BUF;
+      qh = at;
+      kh = qh + TP * QP;
+      v = at;                                            // u after the last slab
+      vl = v + TP * VP;
+      at += 2 * TP * (QP > VP ? QP : VP);
+      a = at;
+      at += TP * AP * 4;
+    } else {
+      overlay = TP > 48 && 2 * TP * QP >= 2 * BUF;
+      ring = at;
+      if (!overlay) at += 2 * BUF;
+      kh = at;
+      at += TP * QP;
+      kl = at;
+      at += TP * QP;
+      qh = at;
+      at += TP * QP;
+      ql = at;
+      at += TP * QP;
+      v = at;
+      at += TP * VP;
+    }
+    wh = at;
+    at += TP * WP;
+    wl = at;
+    at += TP * WP;
+    mask = at;
+    at += TP * 8;
+    depth = at;
+    at += TP * 4;
+    up = at;
+    at += TP * 4;
+    pw = at;
+    at += (kTreeMax + 4) * 4;
+    zq = at;
+    at += TP * 4;
+    den = at;
+    at += 4 * TP * 4;
+    rden = at;
+    at += TP * 4;
+    bad = at;
+    at += 16;
+    bar = at;
+    at += 32;
+    total = at;
+  }
+};
+
+template <int DK, int DV, bool kDelta>
+__global__ void __launch_bounds__(2 * DV + 32, DV == 128 ? 2 : 3)
+tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restrict__ S, const float* __restrict__ z,
+                 const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
+                 const __nv_bfloat16* __restrict__ v, const int* __restrict__ parent, const int* __restrict__ count,
+                 __nv_bfloat16* __restrict__ out, int H, int ntok, const float* __restrict__ alpha, float eps,
+                 int* status) {
+  using Sh = Wide<DK, DV, kDelta>;
+  constexpr int NT = Sh::NT, NW = Sh::NW, SLABS = Sh::SLABS, BUF = Sh::BUF, QP = Sh::QP, VP = Sh::VP, WP = Sh::WP,
+                RP = Sh::RP, AP = Sh::AP, KS = DK / 16, NTM = TM / 8;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const long long bh = blockIdx.x;
+  const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = clamp_count(count, b, ntok);
+  if (n == 0) return;
+  if ((sm100::smem_u32(sm) & 1023u) != 0u) {       // the swizzle goes by address bits
+    if (tid == 0) atomicExch(status, (int)LA_ERR_TIMEOUT);
+    return;
+  }
+  const Sh L((ntok + 15) & ~15);
+  const int TP = (n + 15) & ~15, tiles = (n + 7) >> 3, blocks = TP / 16;
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(sm + L.mask);
+  unsigned int* bad = reinterpret_cast<unsigned int*>(sm + L.bad);
+  int* depth = reinterpret_cast<int*>(sm + L.depth);
+  float* pw = reinterpret_cast<float*>(sm + L.pw);
+  float* zqs = reinterpret_cast<float*>(sm + L.zq);
+  float* den = reinterpret_cast<float*>(sm + L.den);     // [block of j][i]: sums of W over a tile
+  float* rden = reinterpret_cast<float*>(sm + L.rden);
+  float* R = reinterpret_cast<float*>(sm + L.r);
+  float* A = reinterpret_cast<float*>(sm + L.a);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bar);
+  uint64_t* empty = full + 2;
+  const uint32_t base = sm100::smem_u32(sm);
+  const __nv_bfloat16* qb = q + bh * (long long)ntok * DK;
+  const __nv_bfloat16* kb = k + bh * (long long)ntok * DK;
+  const __nv_bfloat16* vb = v + bh * (long long)ntok * DV;
+  __nv_bfloat16* ob = out + bh * (long long)ntok * DV;
+  const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+  int odd_values = 0;
+
+  auto load_slab = [&](int s) {                    // lane 0 of the extra warp
+    uint64_t* bar = full + (s & 1);
+    sm100::mbar_arrive_expect_tx(bar, BUF);
+    for (int x = 0; x < DV / 32; ++x)
+      sm100::tma_load_3d(sm + L.ring + (s & 1) * BUF + x * (SLAB * 128), &map_s, bar, 32 * x, SLAB * s, (int)bh);
+  };
+
+  if (warp == NW) {
+    if (lane == 0) {
+      sm100::mbar_init(full, 1);
+      sm100::mbar_init(full + 1, 1);
+      sm100::mbar_init(empty, NW);
+      sm100::mbar_init(empty + 1, NW);
+      sm100::fence_mbar_init();
+      if (L.overlay) {
+        prefetch_l2(S + bh * (long long)(DK * DV), DK * DV * 4);
+      } else {
+        load_slab(0);
+        if (SLABS > 1) load_slab(1);
+      }
+      bad[0] = bad[1] = 0u;
+    }
+    __syncwarp();
+    tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, reinterpret_cast<int*>(sm + L.up));
+    if (!kDelta && alpha != nullptr)
+      for (int d = lane; d <= kTreeMax; d += 32) pw[d] = tree_power(alpha[h], d);
+  } else {
+    // ---- rows
+    constexpr int CH = DK / 8, RPP = NT / CH, CHV = DV / 8, RPV = NT / CHV;
+    const int ch = tid % CH, chv = tid % CHV;
+    int i = tid / CH, iv = tid / CHV;
+    auto load_qk = [&](int row, uint4& a, uint4& c) {
+      a = c = zero4;
+      if (row < n) {
+        a = *reinterpret_cast<const uint4*>(qb + row * DK + 8 * ch);
+        c = *reinterpret_cast<const uint4*>(kb + row * DK + 8 * ch);
+      }
+    };
+    uint4 xq, xk;
+    load_qk(i, xq, xk);
+    if constexpr (kDelta) {
+      for (; i < TP; i += RPP) {
+        uint4 nq, nk;
+        load_qk(i + RPP, nq, nk);
+        *reinterpret_cast<uint4*>(sm + L.qh + i * QP + 16 * ch) = xq;
+        *reinterpret_cast<uint4*>(sm + L.kh + i * QP + 16 * ch) = xk;
+        xq = nq;
+        xk = nk;
+      }
+    } else {
+      uint4 xv[2];
+      xv[0] = iv < n ? *reinterpret_cast<const uint4*>(vb + iv * DV + 8 * chv) : zero4;
+      float zz[8];
+      const float4 z0 = *reinterpret_cast<const float4*>(z + bh * DK + 8 * ch);
+      const float4 z1 = *reinterpret_cast<const float4*>(z + bh * DK + 8 * ch + 4);
+      zz[0] = z0.x; zz[1] = z0.y; zz[2] = z0.z; zz[3] = z0.w;
+      zz[4] = z1.x; zz[5] = z1.y; zz[6] = z1.z; zz[7] = z1.w;
+      for (int i0 = 0; i0 < TP; i0 += RPP, i += RPP) {       // the same number of passes for every lane
+        uint4 nq, nk, o[4];
+        load_qk(i + RPP, nq, nk);
+        float zq = feature_rows(xq, xk, zz, o);
+        if (i < TP) {
+          *reinterpret_cast<uint4*>(sm + L.qh + i * QP + 16 * ch) = o[0];
+          *reinterpret_cast<uint4*>(sm + L.ql + i * QP + 16 * ch) = o[1];
+          *reinterpret_cast<uint4*>(sm + L.kh + i * QP + 16 * ch) = o[2];
+          *reinterpret_cast<uint4*>(sm + L.kl + i * QP + 16 * ch) = o[3];
+        }
+#pragma unroll
+        for (int off = 1; off < CH; off <<= 1) zq += __shfl_xor_sync(0xffffffffu, zq, off);
+        if (ch == 0 && i < TP) zqs[i] = zq;
+        xq = nq;
+        xk = nk;
+      }
+      for (; iv < TP; iv += RPV) {
+        xv[1] = iv + RPV < n ? *reinterpret_cast<const uint4*>(vb + (iv + RPV) * DV + 8 * chv) : zero4;
+        odd_values |= clear_nonfinite(xv[0]);
+        store_columns(sm + L.v + iv * VP, chv, xv[0]);
+        xv[0] = xv[1];
+      }
+    }
+  }
+  unsigned long long spoilt = 0ull;
+  if (__syncthreads_or(odd_values)) {
+    for (int x = tid; x < n * DV; x += NT + 32)
+      if (nonfinite(__bfloat162float(vb[x]))) atomicOr(bad + ((x / DV) >> 5), 1u << ((x / DV) & 31));
+    __syncthreads();
+    spoilt = (unsigned long long)bad[0] | ((unsigned long long)bad[1] << 32);
+  }
+
+  const int g = lane >> 2, t = lane & 3;
+  // lane's row address of a 16 x 16 block as four 8 x 8 matrices: (rows 0-7,
+  // k 0-7), (rows 8-15, k 0-7), (rows 0-7, k 8-15), (rows 8-15, k 8-15)
+  const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lcol = (lane >> 4) * 16;
+  const uint32_t frag = base + lrow * QP + lcol;
+  if (warp < NW) {
+    // ---- pairs: tiles of 16 nodes i x 16 nodes j, j's block <= i's
+    for (int id = warp; id < blocks * (blocks + 1) / 2; id += NW) {
+      int mi = 0;
+      while ((mi + 1) * (mi + 2) / 2 <= id) ++mi;
+      const int mj = id - mi * (mi + 1) / 2;
+      const uint32_t qa0 = frag + L.qh + 16 * mi * QP, ka0 = frag + L.kh + 16 * mj * QP;
+      float d[2][4] = {}, d2[2][4] = {};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t qa[4], kb4[4], x4[4], y4[4];
+        ldmatrix4(qa, qa0 + 32 * ks);
+        ldmatrix4(kb4, ka0 + 32 * ks);
+        mma(d[0], qa, kb4[0], kb4[2]);
+        mma(d[1], qa, kb4[1], kb4[3]);
+        if constexpr (kDelta) {
+          ldmatrix4(x4, frag + L.kh + 16 * mi * QP + 32 * ks);
+          mma(d2[0], x4, kb4[0], kb4[2]);
+          mma(d2[1], x4, kb4[1], kb4[3]);
+        } else {
+          ldmatrix4(x4, ka0 + (L.kl - L.kh) + 32 * ks);
+          ldmatrix4(y4, qa0 + (L.ql - L.qh) + 32 * ks);
+          mma(d2[0], qa, x4[0], x4[2]);
+          mma(d2[1], qa, x4[1], x4[3]);
+          mma(d2[0], y4, kb4[0], kb4[2]);
+          mma(d2[1], y4, kb4[1], kb4[3]);
+        }
+      }
+      // lane: rows 16 mi + g (+ 8), columns 16 mj + 8 nj + 2t (+ 1)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 16 * mi + g + 8 * e, dr = depth[row];
+        const unsigned long long m = mask[row];
+        float sum = 0.f;
+#pragma unroll
+        for (int nj = 0; nj < 2; ++nj) {
+          const int col = 16 * mj + 8 * nj + 2 * t;
+          const bool on0 = (m >> col) & 1, on1 = (m >> (col + 1)) & 1;
+          float w0 = d[nj][2 * e], w1 = d[nj][2 * e + 1];
+          if constexpr (kDelta) {
+            A[col * AP + row] = on0 && row != col ? d2[nj][2 * e] : 0.f;
+            A[(col + 1) * AP + row] = on1 && row != col + 1 ? d2[nj][2 * e + 1] : 0.f;
+          } else {
+            w0 += d2[nj][2 * e];
+            w1 += d2[nj][2 * e + 1];
+            if (alpha != nullptr) {
+              w0 *= pw[max(dr - depth[col], 0)];
+              w1 *= pw[max(dr - depth[col + 1], 0)];
+            }
+          }
+          w0 = on0 ? w0 : 0.f;
+          w1 = on1 ? w1 : 0.f;
+          sum += w0 + w1;
+          uint32_t hi, lo;
+          split2(w0, w1, hi, lo);
+          *reinterpret_cast<uint32_t*>(sm + L.wh + row * WP + 2 * col) = hi;
+          *reinterpret_cast<uint32_t*>(sm + L.wl + row * WP + 2 * col) = lo;
+        }
+        if constexpr (!kDelta) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          if (t == 0) den[mj * TP + row] = sum;
+        }
+      }
+    }
+  }
+  if (!kDelta) {                                   // (the delta rule's pairs and its read share nothing but q and k)
+    // the buffers were ordinary memory until here, the copies' next
+    if (L.overlay) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+  }
+
+  // ---- read: D[c][i] = sum_r S[r][c] x_i[r], slab by slab
+  float acc[NTM][4], acck[kDelta ? NTM : 1][4];
+#pragma unroll
+  for (int nt = 0; nt < NTM; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc[nt][e] = 0.f;
+      if (kDelta) acck[nt][e] = 0.f;
+    }
+  const int c0 = 16 * warp + 2 * g;                // this lane's columns: c0, c0 + 1
+  if (warp == NW) {
+    if (lane == 0) {
+      if (L.overlay) {
+        load_slab(0);
+        if (SLABS > 1) load_slab(1);
+      }
+      for (int s = 2; s < SLABS; ++s) {
+        if (!sm100::mbar_drain(empty + (s & 1), ((s >> 1) - 1) & 1, kWaitNs)) atomicExch(status, (int)LA_ERR_TIMEOUT);
+        load_slab(s);
+      }
+      // nothing in flight when the CTA ends, whatever became of the others
+      for (int s = SLABS > 1 ? SLABS - 2 : 0; s < SLABS; ++s)
+        if (!sm100::mbar_drain(full + (s & 1), (s >> 1) & 1, kWaitNs)) atomicExch(status, (int)LA_ERR_TIMEOUT);
+    }
+    __syncwarp();
+    if (!kDelta)
+      for (int i = lane; i < n; i += 32) {
+        float x = zqs[i];
+        if (alpha != nullptr) x *= pw[depth[i]];
+        for (int mj = 0; mj <= i / 16; ++mj) x += den[mj * TP + i];
+        rden[i] = 1.f / (x + eps);
+      }
+  } else {
+    // rows 2t and 2t + 1 of a step (2t + 8 and 2t + 9 likewise): the 16-byte
+    // piece of column c0 lies at its index XOR the row's low three bits
+    const int piece = (warp & 1) * 4 + (g >> 1);
+    const uint8_t* box = sm + L.ring + (warp >> 1) * (SLAB * 128) + (g & 1) * 8;
+    const uint8_t* even = box + 2 * t * 128 + ((piece ^ (2 * t)) << 4);
+    const uint8_t* odd = box + (2 * t + 1) * 128 + ((piece ^ (2 * t + 1)) << 4);
+#pragma unroll 1
+    for (int s = 0; s < SLABS; ++s) {
+      (void)sm100::mbar_drain(full + (s & 1), (s >> 1) & 1, kWaitNs);
+#pragma unroll
+      for (int kk = 0; kk < SLAB / 16; ++kk) {
+        const int at = (s & 1) * BUF + 2048 * kk;
+        const float2 s0 = *reinterpret_cast<const float2*>(even + at);
+        const float2 s1 = *reinterpret_cast<const float2*>(odd + at);
+        const float2 s2 = *reinterpret_cast<const float2*>(even + at + 1024);
+        const float2 s3 = *reinterpret_cast<const float2*>(odd + at + 1024);
+        uint32_t ah[4], al[4];
+        split2(s0.x, s1.x, ah[0], al[0]);
+        split2(s0.y, s1.y, ah[1], al[1]);
+        split2(s2.x, s3.x, ah[2], al[2]);
+        split2(s2.y, s3.y, ah[3], al[3]);
+        const uint32_t xa = frag + 32 * (s * (SLAB / 16) + kk);
+#pragma unroll
+        for (int ib = 0; ib < NTM / 2; ++ib)
+          if (ib < blocks) {
+            uint32_t x4[4];
+            ldmatrix4(x4, xa + L.qh + 16 * ib * QP);
+            mma(acc[2 * ib], ah, x4[0], x4[2]);
+            mma(acc[2 * ib + 1], ah, x4[1], x4[3]);
+            mma(acc[2 * ib], al, x4[0], x4[2]);
+            mma(acc[2 * ib + 1], al, x4[1], x4[3]);
+            if constexpr (kDelta) {
+              ldmatrix4(x4, xa + L.kh + 16 * ib * QP);
+              mma(acck[2 * ib], ah, x4[0], x4[2]);
+              mma(acck[2 * ib + 1], ah, x4[1], x4[3]);
+              mma(acck[2 * ib], al, x4[0], x4[2]);
+              mma(acck[2 * ib + 1], al, x4[1], x4[3]);
+            } else {
+              ldmatrix4(x4, xa + L.ql + 16 * ib * QP);
+              mma(acc[2 * ib], ah, x4[0], x4[2]);
+              mma(acc[2 * ib + 1], ah, x4[1], x4[3]);
+            }
+          }
+      }
+      __syncwarp();
+      if (lane == 0 && s + 2 < SLABS) sm100::mbar_arrive(empty + (s & 1));
+    }
+  }
+  __syncthreads();
+
+  if constexpr (kDelta) {
+    // ---- R = v - S^T k where the slabs were
+    if (warp < NW) {
+#pragma unroll
+      for (int nt = 0; nt < NTM; ++nt)
+        if (nt < tiles) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = 8 * nt + 2 * t + e;
+            const uint32_t x = j < n ? *reinterpret_cast<const uint32_t*>(vb + j * DV + c0) : 0u;
+            *reinterpret_cast<float2*>(R + j * RP + c0) =
+                make_float2(low_half(x) - acck[nt][e], high_half(x) - acck[nt][2 + e]);
+          }
+        }
+    }
+    __syncthreads();
+    // ---- u_j = R_j - sum_{l on j's path} (k_j.k_l) u_l: two lanes per
+    // column, blocks of 8 nodes: the earlier nodes' part first (each lane
+    // every other node, 8 sums at a time), then the block's own triangle.
+    // `off`: earlier nodes whose u is not finite in this column; while there
+    // is none, the zeros of A leave the other paths out.
+    if (warp < NW) {
+      const int c = tid >> 1, half = tid & 1;
+      unsigned long long off = 0ull;
+      for (int j0 = 0; j0 < TP; j0 += 8) {
+        float u[8];
+        if (j0 < n) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = half == 0 ? R[(j0 + e) * RP + c] : 0.f;
+#pragma unroll 2
+          for (int l = half; l < j0; l += 2) {
+            const float ul = R[l * RP + c];
+            const float4 a0 = *reinterpret_cast<const float4*>(A + l * AP + j0);
+            const float4 a1 = *reinterpret_cast<const float4*>(A + l * AP + j0 + 4);
+            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            if (!((off >> l) & 1)) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) u[e] = fmaf(-av[e], ul, u[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if ((mask[j0 + e] >> l) & 1) u[e] = fmaf(-av[e], ul, u[e]);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] += __shfl_xor_sync(0xffffffffu, u[e], 1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int l = 0; l < e; ++l) {
+              const float x = fmaf(-A[(j0 + l) * AP + j0 + e], u[l], u[e]);
+              u[e] = (mask[j0 + e] >> (j0 + l)) & 1 ? x : u[e];
+            }
+            if (j0 + e >= n) u[e] = 0.f;
+            if (nonfinite(u[e])) off |= 1ull << (j0 + e);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = 0.f;
+        }
+        const int at = (c >> 4) * 32 + (c & 1) * 16 + ((c & 15) >> 1) * 2;   // even columns of a block first
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((e & 1) == half) {
+            const int j = j0 + e;
+            R[j * RP + c] = u[e];
+            const float x = nonfinite(u[e]) ? 0.f : u[e];
+            const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+            *reinterpret_cast<__nv_bfloat16*>(sm + L.v + j * VP + at) = hi;
+            *reinterpret_cast<__nv_bfloat16*>(sm + L.vl + j * VP + at) = __float2bfloat16_rn(x - __bfloat162float(hi));
+          }
+        __syncwarp();
+      }
+      if (off & 0xffffffffull) atomicOr(bad, (unsigned int)off);
+      if (off >> 32) atomicOr(bad + 1, (unsigned int)(off >> 32));
+    }
+    __syncthreads();
+    spoilt = (unsigned long long)bad[0] | ((unsigned long long)bad[1] << 32);
+  }
+  if (warp >= NW) return;
+
+  if (!kDelta && alpha != nullptr) {
+    // the read's part of a node decays along its whole path
+#pragma unroll
+    for (int nt = 0; nt < NTM; ++nt)
+      if (nt < tiles) {
+        const float p0 = pw[depth[8 * nt + 2 * t]], p1 = pw[depth[8 * nt + 2 * t + 1]];
+        acc[nt][0] *= p0;
+        acc[nt][1] *= p1;
+        acc[nt][2] *= p0;
+        acc[nt][3] *= p1;
+      }
+  }
+
+  // ---- path: D[c][i] += sum_j V[j][c] W[i][j], j in steps of 16
+  {
+    const int mat = lane >> 3, rr = lane & 7;
+    const uint32_t va = base + L.v + (rr + (mat >> 1) * 8) * VP + 32 * warp + (mat & 1) * 16;
+    const uint32_t wa = base + L.wh + lrow * WP + lcol;
+#pragma unroll
+    for (int js = 0; js < NTM / 2; ++js)
+      if (js < blocks) {
+        uint32_t a[4], al[4];
+        ldmatrix4t(a, va + js * 16 * VP);
+        if constexpr (kDelta) ldmatrix4t(al, va + (L.vl - L.v) + js * 16 * VP);
+#pragma unroll
+        for (int ib = js; ib < NTM / 2; ++ib)
+          if (ib < blocks) {
+            uint32_t wh[4], wl[4];
+            ldmatrix4(wh, wa + ib * 16 * WP + 32 * js);
+            ldmatrix4(wl, wa + (L.wl - L.wh) + ib * 16 * WP + 32 * js);
+            mma(acc[2 * ib], a, wh[0], wh[2]);
+            mma(acc[2 * ib + 1], a, wh[1], wh[3]);
+            mma(acc[2 * ib], a, wl[0], wl[2]);
+            mma(acc[2 * ib + 1], a, wl[1], wl[3]);
+            if constexpr (kDelta) {
+              mma(acc[2 * ib], al, wh[0], wh[2]);
+              mma(acc[2 * ib + 1], al, wh[1], wh[3]);
+            }
+          }
+      }
+  }
+
+  // ---- out: lane holds nodes 8 nt + 2t (+ 1), columns c0, c0 + 1
+#pragma unroll
+  for (int nt = 0; nt < NTM; ++nt)
+    if (nt < tiles) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int node = 8 * nt + 2 * t + e;
+        if (node >= n) continue;
+        float o0 = acc[nt][e], o1 = acc[nt][2 + e];
+        if (spoilt != 0ull) {
+          for (unsigned long long m = mask[node] & spoilt; m != 0ull; m &= m - 1) {
+            const int j = __ffsll((long long)m) - 1;
+            float x0, x1;
+            if constexpr (kDelta) {
+              x0 = R[j * RP + c0];
+              x1 = R[j * RP + c0 + 1];
+            } else {
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(vb + j * DV + c0);
+              x0 = low_half(x);
+              x1 = high_half(x);
+            }
+            const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L.wh + node * WP + 2 * j)) +
+                            __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L.wl + node * WP + 2 * j));
+            if (nonfinite(x0)) o0 = fmaf(w, x0, o0);
+            if (nonfinite(x1)) o1 = fmaf(w, x1, o1);
+          }
+        }
+        if constexpr (!kDelta) {
+          o0 *= rden[node];
+          o1 *= rden[node];
+        }
+        *reinterpret_cast<uint32_t*>(ob + (long long)node * DV + c0) = pack2(o0, o1);
+      }
+    }
+}
+
+template <int DK, int DV, bool kDelta>
+cudaError_t launch(const TreeArgs& a) {
+  using Sh = Wide<DK, DV, kDelta>;
+  constexpr Sh most(TM), middle(48);
+  // two CTAs per SM (228 KiB, 1 KiB of it taken by each CTA)
+  static_assert(most.total + 1024 <= 116736 && middle.total + 1024 <= 116736, "shared memory of two CTAs");
+  static_assert(most.ring % 1024 == 0, "the swizzle goes by address bits");
+  const Sh L((a.T + 15) & ~15);
+  auto kern = tree_wide_kernel<DK, DV, kDelta>;
+  static KernelOnce once;
+  int resident = 0;
+  cudaError_t e = once.prepare(kern, Sh::NT + 32, most.total > middle.total ? most.total : middle.total, &resident);
+  if (e != cudaSuccess) return e;
+  int* status = device_status_ptr();
+  if (status == nullptr) return cudaErrorNotReady;
+  CUtensorMap map_s;
+  e = state_map<DK, DV>(&map_s, a.S, a.BH, SLAB);
+  if (e != cudaSuccess) return e;
+  kern<<<a.BH, Sh::NT + 32, L.total, a.stream>>>(map_s, a.S, a.z, (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.k,
+                                                 (const __nv_bfloat16*)a.v, a.parent, a.count, (__nv_bfloat16*)a.out,
+                                                 a.H, a.T, a.alpha, a.eps, status);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+}  // namespace treewide
+}  // namespace la
