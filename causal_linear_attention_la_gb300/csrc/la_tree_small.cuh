@@ -19,8 +19,8 @@
 //           thread per pair, which applies mask and decay and stores W as hi
 //           and lo; 1 / den
 //   read    D = S^T x, then D += V^T W^T, out
-// The delta rule reads for the keys before the queries and solves for u in
-// registers, a thread per column.
+// The delta rule reads for the keys as well and multiplies by the inverse
+// triangle before the path.
 #pragma once
 
 #include "la_tree_ops.cuh"
@@ -41,21 +41,20 @@ struct Small {
   static constexpr int BOX = DK * 128;                   // bytes of one box of the state: dk rows x 32 columns
   static constexpr int QP = 2 * DK + 16;                 // bytes per row of q, k (matrix loads without bank conflicts)
   static constexpr int VP = 2 * DV + 16;                 // bytes per row of v, u
-  static constexpr int RP = DV + 8;                      // floats per row of R
   static constexpr int S = 0;
   static constexpr int QH = S + DK * DV * 4;
   static constexpr int QL = QH + TP * QP;
   static constexpr int KH = QL + (kDelta ? 0 : TP * QP);
   static constexpr int KL = KH + TP * QP;
-  static constexpr int V = kDelta ? KL : KL + TP * QP;
-  static constexpr int VL = V + TP * VP;                 // delta: u's low part
-  static constexpr int PART = VL + (kDelta ? TP * VP : 0);
+  static constexpr int V = KL + (kDelta ? 0 : TP * QP);
+  static constexpr int PART = V + (kDelta ? 0 : TP * VP);
   static constexpr int PART2 = PART + KW * TP * PP * 4;  // delta: k_j . k_l
-  static constexpr int R = PART2 + (kDelta ? KW * TP * PP * 4 : 0);
-  static constexpr int A = R + (kDelta ? TP * RP * 4 : 0);
+  static constexpr int A = PART2 + (kDelta ? KW * TP * PP * 4 : 0);
   static constexpr int WH = A + (kDelta ? TP * TP * 4 : 0);
   static constexpr int WL = WH + TP * WPB;
-  static constexpr int MASK = WL + TP * WPB;
+  static constexpr int LH = WL + TP * WPB;               // delta: the inverse triangle
+  static constexpr int LL = LH + (kDelta ? TP * WPB : 0);
+  static constexpr int MASK = LL + (kDelta ? TP * WPB : TP * 0);
   static constexpr int DEPTH = MASK + TP * 8;
   static constexpr int UP = DEPTH + TP * 4;
   static constexpr int PW = UP + TP * 4;
@@ -64,7 +63,8 @@ struct Small {
   static constexpr int BAD = RDEN + TP * 4;
   static constexpr int BAR = BAD + 16;
   static constexpr int BYTES = BAR + 16;
-  static_assert(QH % 16 == 0 && PART % 16 == 0 && R % 16 == 0 && A % 16 == 0 && MASK % 16 == 0 && BAR % 8 == 0, "alignment");
+  static_assert(QH % 16 == 0 && PART % 16 == 0 && A % 16 == 0 && WH % 16 == 0 && LH % 16 == 0 && MASK % 16 == 0 && BAR % 8 == 0, "alignment");
+  static_assert(TP * (2 * (TP + 1) + DV) * 4 <= MASK, "room for delta_tree_by_paths");
   // two CTAs per SM (228 KiB, 1 KiB of it taken by each CTA)
   static_assert(BYTES + 1024 <= 116736, "shared memory of two CTAs");
 };
@@ -76,7 +76,7 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
                   const int* __restrict__ parent, const int* __restrict__ count, __nv_bfloat16* __restrict__ out, int H,
                   int ntok, const float* __restrict__ alpha, float eps, int* status) {
   using L = Small<DK, DV, kDelta>;
-  constexpr int NT = L::NT, NW = L::NW, KS = L::KS, KW = L::KW, BOX = L::BOX, QP = L::QP, VP = L::VP, RP = L::RP;
+  constexpr int NT = L::NT, NW = L::NW, KS = L::KS, KW = L::KW, BOX = L::BOX, QP = L::QP, VP = L::VP;
   extern __shared__ __align__(1024) uint8_t sm[];
   const long long bh = blockIdx.x;
   const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -160,7 +160,7 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
         }
 #pragma unroll
         for (int off = 1; off < CH; off <<= 1) zq += __shfl_xor_sync(0xffffffffu, zq, off);
-        if (ch == 0 && i < TP) zqs[i] = zq;
+        if (i < TP) zqs[i] = zq;                     // the same number from every lane of the row: no divergence
       }
       odd_values = clear_nonfinite(xv);
       store_columns(sm + L::V + iv * VP, chv, xv);
@@ -263,17 +263,28 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
       }
     }
   }
+  if constexpr (kDelta) {
+    __syncthreads();
+    if (warp == NW && lane < TP)
+      invert_unit_triangle(reinterpret_cast<const float*>(sm + L::A), lane, sm + L::LH, sm + L::LL, WPB);
+  }
 
   // ---- read: D[c][i] = sum_r S[r][c] x_i[r]
   const bool here = sm100::mbar_drain(bar, 0, kWaitNs);
   if (!here && lane == 0) atomicExch(status, (int)LA_ERR_TIMEOUT);
   const int c0 = 16 * warp + 2 * g;
-  float acc[2][4];
-  auto read_state = [&](int hi_off, int lo_off) {
+  float acc[2][4] = {}, acck[2][4] = {};           // (acck: delta rule)
+  uint32_t vr[2][2];                               // delta: this lane's values of v
+  if (warp < NW) {
+    if constexpr (kDelta) {
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          const int j = 8 * nt + 2 * t + e;
+          vr[nt][e] = j < n ? *reinterpret_cast<const uint32_t*>(vb + j * DV + c0) : 0u;
+        }
+    }
     // rows 2t and 2t + 1 of a step (2t + 8 and 2t + 9 likewise): the 16-byte
     // piece of column c0 lies at its index XOR the row's low three bits
     const int piece = (warp & 1) * 4 + (g >> 1);
@@ -287,88 +298,49 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
       const float2 s1 = *reinterpret_cast<const float2*>(odd + 2048 * ks);
       const float2 s2 = *reinterpret_cast<const float2*>(even + 2048 * ks + 1024);
       const float2 s3 = *reinterpret_cast<const float2*>(odd + 2048 * ks + 1024);
-      uint32_t ah[4], al[4], bh4[4], bl4[4];
+      uint32_t ah[4], al[4], x4[4], y4[4];
       split2(s0.x, s1.x, ah[0], al[0]);
       split2(s0.y, s1.y, ah[1], al[1]);
       split2(s2.x, s3.x, ah[2], al[2]);
       split2(s2.y, s3.y, ah[3], al[3]);
-      ldmatrix4(bh4, xa + hi_off + 32 * ks);
-      mma(acc[0], ah, bh4[0], bh4[2]);
-      mma(acc[0], al, bh4[0], bh4[2]);
+      ldmatrix4(x4, xa + L::QH + 32 * ks);
+      ldmatrix4(y4, xa + (kDelta ? L::KH : L::QL) + 32 * ks);
+      mma(acc[0], ah, x4[0], x4[2]);
+      mma(acc[0], al, x4[0], x4[2]);
+      mma(kDelta ? acck[0] : acc[0], ah, y4[0], y4[2]);
+      if constexpr (kDelta) mma(acck[0], al, y4[0], y4[2]);
       if (tiles > 1) {
-        mma(acc[1], ah, bh4[1], bh4[3]);
-        mma(acc[1], al, bh4[1], bh4[3]);
-      }
-      if constexpr (!kDelta) {
-        ldmatrix4(bl4, xa + lo_off + 32 * ks);
-        mma(acc[0], ah, bl4[0], bl4[2]);
-        if (tiles > 1) mma(acc[1], ah, bl4[1], bl4[3]);
+        mma(acc[1], ah, x4[1], x4[3]);
+        mma(acc[1], al, x4[1], x4[3]);
+        mma(kDelta ? acck[1] : acc[1], ah, y4[1], y4[3]);
+        if constexpr (kDelta) mma(acck[1], al, y4[1], y4[3]);
       }
     }
-  };
-  float* R = reinterpret_cast<float*>(sm + L::R);
-  if (warp < NW) {
-    if constexpr (kDelta) {
-      uint32_t vr[2][2];
+  }
+  __syncthreads();                                 // W, 1 / den, the inverse triangle
+
+  uint32_t a[4], al[4];                            // v or u as the A operand
+  if constexpr (kDelta) {
+    int odd_u = 0;
+    if (warp < NW) {
+      const uint32_t la = base + L::LH + lrow * WPB + lcol;
+      float u[2][4] = {};
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = 8 * nt + 2 * t + e;
-          vr[nt][e] = j < n ? *reinterpret_cast<const uint32_t*>(vb + j * DV + c0) : 0u;
+          acck[nt][e] = low_half(vr[nt][e]) - acck[nt][e];
+          acck[nt][2 + e] = high_half(vr[nt][e]) - acck[nt][2 + e];
         }
-      read_state(L::KH, 0);
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float2*>(R + (8 * nt + 2 * t + e) * RP + c0) =
-              make_float2(low_half(vr[nt][e]) - acc[nt][e], high_half(vr[nt][e]) - acc[nt][2 + e]);
+      as_operand(acck[0], acck[1], a, al);
+      mma_block(u[0], u[1], a, al, la, la + (L::LL - L::LH));
+      odd_u = any_nonfinite(u[0]) || any_nonfinite(u[1]);
+      as_operand(u[0], u[1], a, al);
     }
-    read_state(L::QH, L::QL);
-  }
-  __syncthreads();
-
-  if constexpr (kDelta) {
-    // ---- u_j = R_j - sum_{l on j's path} (k_j.k_l) u_l, a thread per column
-    if (tid < DV) {
-      const int c = tid;
-      const float* A = reinterpret_cast<const float*>(sm + L::A);
-      unsigned int off = 0u;
-      float u[TP];
-#pragma unroll
-      for (int j = 0; j < TP; ++j) u[j] = R[j * RP + c];
-#pragma unroll
-      for (int j = 0; j < TP; ++j) {
-        if (off == 0u) {
-#pragma unroll
-          for (int l = 0; l < j; ++l) u[j] = fmaf(-A[j * TP + l], u[l], u[j]);
-        } else {
-          // a node above with a value that is not finite: the zeros of A no
-          // longer leave the other paths out
-          const unsigned int m = (unsigned int)mask[j];
-#pragma unroll
-          for (int l = 0; l < j; ++l) {
-            const float x = fmaf(-A[j * TP + l], u[l], u[j]);
-            u[j] = (m >> l) & 1 ? x : u[j];
-          }
-        }
-        if (j >= n) u[j] = 0.f;
-        if (nonfinite(u[j])) off |= 1u << j;
-      }
-      const int at = (c >> 4) * 32 + (c & 1) * 16 + ((c & 15) >> 1) * 2;   // even columns of a block first
-#pragma unroll
-      for (int j = 0; j < TP; ++j) {
-        if (off != 0u) R[j * RP + c] = u[j];
-        const float x = nonfinite(u[j]) ? 0.f : u[j];
-        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-        *reinterpret_cast<__nv_bfloat16*>(sm + L::V + j * VP + at) = hi;
-        *reinterpret_cast<__nv_bfloat16*>(sm + L::VL + j * VP + at) = __float2bfloat16_rn(x - __bfloat162float(hi));
-      }
-      if (off != 0u) atomicOr(bad, off);
+    if (__syncthreads_or(odd_u)) {
+      delta_tree_by_paths<DK, DV>(S + bh * (long long)(DK * DV), qb, kb, vb, ob, mask, n, reinterpret_cast<float*>(sm));
+      return;
     }
-    __syncthreads();
-    spoilt = bad[0];
   }
   if (warp >= NW) return;
 
@@ -385,54 +357,45 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
   }
   // ---- path: D[c][i] += sum_j V[j][c] W[i][j]
   {
-    const int mat = lane >> 3, rr = lane & 7;
-    uint32_t a[4], al[4], wh[4], wl[4];
-    const uint32_t va = base + L::V + (rr + (mat >> 1) * 8) * VP + 32 * warp + (mat & 1) * 16;
-    ldmatrix4t(a, va);
     const uint32_t wa = base + L::WH + lrow * WPB + lcol;
-    ldmatrix4(wh, wa);
-    ldmatrix4(wl, wa + (L::WL - L::WH));
-    mma(acc[0], a, wh[0], wh[2]);
-    mma(acc[0], a, wl[0], wl[2]);
-    mma(acc[1], a, wh[1], wh[3]);
-    mma(acc[1], a, wl[1], wl[3]);
     if constexpr (kDelta) {
-      ldmatrix4t(al, va + (L::VL - L::V));
-      mma(acc[0], al, wh[0], wh[2]);
-      mma(acc[1], al, wh[1], wh[3]);
+      mma_block(acc[0], acc[1], a, al, wa, wa + (L::WL - L::WH));
+    } else {
+      uint32_t wh[4], wl[4];
+      ldmatrix4t(a, base + L::V + ((lane & 7) + (lane >> 4) * 8) * VP + 32 * warp + ((lane >> 3) & 1) * 16);
+      ldmatrix4(wh, wa);
+      ldmatrix4(wl, wa + (L::WL - L::WH));
+      mma(acc[0], a, wh[0], wh[2]);
+      mma(acc[1], a, wh[1], wh[3]);
+      mma(acc[0], a, wl[0], wl[2]);
+      mma(acc[1], a, wl[1], wl[3]);
     }
   }
   // ---- out
+  if (!kDelta && spoilt != 0ull) {
+    // the values left out of v, for the nodes below them
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int node = 8 * nt + 2 * t + e;
+        for (unsigned long long m = mask[node] & spoilt; m != 0ull; m &= m - 1) {
+          const int j = __ffsll((long long)m) - 1;
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(vb + j * DV + c0);
+          const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L::WH + node * WPB + 2 * j)) +
+                          __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L::WL + node * WPB + 2 * j));
+          if (nonfinite(low_half(x))) acc[nt][e] = fmaf(w, low_half(x), acc[nt][e]);
+          if (nonfinite(high_half(x))) acc[nt][2 + e] = fmaf(w, high_half(x), acc[nt][2 + e]);
+        }
+      }
+  }
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int node = 8 * nt + 2 * t + e;
-      if (node >= n) continue;
-      float o0 = acc[nt][e], o1 = acc[nt][2 + e];
-      if (spoilt != 0ull) {
-        for (unsigned long long m = mask[node] & spoilt; m != 0ull; m &= m - 1) {
-          const int j = __ffsll((long long)m) - 1;
-          float x0, x1;
-          if constexpr (kDelta) {
-            x0 = R[j * RP + c0];
-            x1 = R[j * RP + c0 + 1];
-          } else {
-            const uint32_t x = *reinterpret_cast<const uint32_t*>(vb + j * DV + c0);
-            x0 = low_half(x);
-            x1 = high_half(x);
-          }
-          const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L::WH + node * WPB + 2 * j)) +
-                          __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L::WL + node * WPB + 2 * j));
-          if (nonfinite(x0)) o0 = fmaf(w, x0, o0);
-          if (nonfinite(x1)) o1 = fmaf(w, x1, o1);
-        }
-      }
-      if constexpr (!kDelta) {
-        o0 *= rden[node];
-        o1 *= rden[node];
-      }
-      *reinterpret_cast<uint32_t*>(ob + node * DV + c0) = pack2(o0, o1);
+      const float r = kDelta ? 1.f : rden[node];
+      if (node < n) *reinterpret_cast<uint32_t*>(ob + node * DV + c0) = pack2(acc[nt][e] * r, acc[nt][2 + e] * r);
     }
 }
 

@@ -22,9 +22,9 @@
 // registers, as fragments of 64 bytes, cost twice the wavefronts and 64
 // registers a thread: 79 us on 1536 decay-gated states of up to 64 nodes.)
 //
-// The delta rule reads for keys and queries in one pass over the slabs (their
-// buffers become R = v - S^T k), solves for u with two lanes a column, in
-// blocks of 8 nodes, and u (hi and lo) takes the place of q and k.
+// The delta rule reads for keys and queries in one pass over the slabs and
+// solves for u in registers (la_tree_ops.cuh) while the extra warp has inverted
+// the diagonal blocks.
 #pragma once
 
 #include "la_tree_ops.cuh"
@@ -44,34 +44,32 @@ struct Wide {
   static constexpr int BUF = SLAB * DV * 4;              // bytes of a slab
   static constexpr int QP = 2 * DK + 16, VP = 2 * DV + 16;
   static constexpr int WP = 2 * TM + 16;
-  static constexpr int RP = DV + 16;                     // floats per row of R: the two lanes of a column in different banks
-  static constexpr int AP = TM + 4;
-  int ring, qh, ql, kh, kl, v, vl, wh, wl, r, a, mask, depth, up, pw, zq, den, rden, bad, bar, total;
+  int ring, qh, ql, kh, kl, v, wh, wl, ah, al, tri, mask, depth, up, pw, zq, den, rden, bad, bar, total;
   bool overlay;                                          // the ring lies where phi(k) was
   __host__ __device__ constexpr explicit Wide(int TP)
-      : ring(0), qh(0), ql(0), kh(0), kl(0), v(0), vl(0), wh(0), wl(0), r(0), a(0), mask(0), depth(0), up(0), pw(0), zq(0),
-        den(0), rden(0), bad(0), bar(0), total(0), overlay(false) {
+      : ring(0), qh(0), ql(0), kh(0), kl(0), v(0), wh(0), wl(0), ah(0), al(0), tri(0), mask(0), depth(0), up(0), pw(0),
+        zq(0), den(0), rden(0), bad(0), bar(0), total(0), overlay(false) {
     int at = 0;
-    if (kDelta) {
-      ring = r = at;                                     // R after the last slab
-      at += TP * RP * 4 > 2 * BUF ? TP * RP * 4 : 2 * BUF;
-      qh = at;
-      kh = qh + TP * QP;
-      v = at;                                            // u after the last slab
-      vl = v + TP * VP;
-      at += 2 * TP * (QP > VP ? QP : VP);
-      a = at;
-      at += TP * AP * 4;
-    } else {
-      overlay = TP > 48 && 2 * TP * QP >= 2 * BUF;
-      ring = at;
-      if (!overlay) at += 2 * BUF;
-      kh = at;
-      at += TP * QP;
+    overlay = !kDelta && TP > 48 && 2 * TP * QP >= 2 * BUF;
+    if (!overlay) at += 2 * BUF;
+    kh = at;
+    at += TP * QP;
+    if (!kDelta) {
       kl = at;
       at += TP * QP;
-      qh = at;
-      at += TP * QP;
+    }
+    qh = at;
+    at += TP * QP;
+    if (kDelta) {
+      // the key products: -A below the diagonal blocks, their inverses on it
+      // (bf16 hi and lo), the diagonal blocks themselves (fp32)
+      ah = at;
+      at += TP * WP;
+      al = at;
+      at += TP * WP;
+      tri = at;
+      at += TP * 16 * 4;
+    } else {
       ql = at;
       at += TP * QP;
       v = at;
@@ -112,7 +110,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
                  int* status) {
   using Sh = Wide<DK, DV, kDelta>;
   constexpr int NT = Sh::NT, NW = Sh::NW, SLABS = Sh::SLABS, BUF = Sh::BUF, QP = Sh::QP, VP = Sh::VP, WP = Sh::WP,
-                RP = Sh::RP, AP = Sh::AP, KS = DK / 16, NTM = TM / 8;
+                KS = DK / 16, NTM = TM / 8;
   extern __shared__ __align__(1024) uint8_t sm[];
   const long long bh = blockIdx.x;
   const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -131,8 +129,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
   float* zqs = reinterpret_cast<float*>(sm + L.zq);
   float* den = reinterpret_cast<float*>(sm + L.den);     // [block of j][i]: sums of W over a tile
   float* rden = reinterpret_cast<float*>(sm + L.rden);
-  float* R = reinterpret_cast<float*>(sm + L.r);
-  float* A = reinterpret_cast<float*>(sm + L.a);
+  float* tri = reinterpret_cast<float*>(sm + L.tri);     // [block][16][16]: A on the diagonal
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bar);
   uint64_t* empty = full + 2;
   const uint32_t base = sm100::smem_u32(sm);
@@ -170,57 +167,70 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
     if (!kDelta && alpha != nullptr)
       for (int d = lane; d <= kTreeMax; d += 32) pw[d] = tree_power(alpha[h], d);
   } else {
-    // ---- rows
+    // ---- rows: batches of up to four passes, all loads of a batch in flight
     constexpr int CH = DK / 8, RPP = NT / CH, CHV = DV / 8, RPV = NT / CHV;
+    constexpr int PB = TM / RPP < 4 ? TM / RPP : 4, PV = 4;
+    static_assert(RPV * PV == TM, "one batch of v");
     const int ch = tid % CH, chv = tid % CHV;
-    int i = tid / CH, iv = tid / CHV;
-    auto load_qk = [&](int row, uint4& a, uint4& c) {
-      a = c = zero4;
-      if (row < n) {
-        a = *reinterpret_cast<const uint4*>(qb + row * DK + 8 * ch);
-        c = *reinterpret_cast<const uint4*>(kb + row * DK + 8 * ch);
+    uint4 xv[PV];
+    if (!kDelta) {
+#pragma unroll
+      for (int p = 0; p < PV; ++p) {
+        const int iv = tid / CHV + p * RPV;
+        xv[p] = iv < n ? *reinterpret_cast<const uint4*>(vb + iv * DV + 8 * chv) : zero4;
       }
-    };
-    uint4 xq, xk;
-    load_qk(i, xq, xk);
-    if constexpr (kDelta) {
-      for (; i < TP; i += RPP) {
-        uint4 nq, nk;
-        load_qk(i + RPP, nq, nk);
-        *reinterpret_cast<uint4*>(sm + L.qh + i * QP + 16 * ch) = xq;
-        *reinterpret_cast<uint4*>(sm + L.kh + i * QP + 16 * ch) = xk;
-        xq = nq;
-        xk = nk;
-      }
-    } else {
-      uint4 xv[2];
-      xv[0] = iv < n ? *reinterpret_cast<const uint4*>(vb + iv * DV + 8 * chv) : zero4;
-      float zz[8];
+    }
+    float zz[8];
+    if (!kDelta) {
       const float4 z0 = *reinterpret_cast<const float4*>(z + bh * DK + 8 * ch);
       const float4 z1 = *reinterpret_cast<const float4*>(z + bh * DK + 8 * ch + 4);
       zz[0] = z0.x; zz[1] = z0.y; zz[2] = z0.z; zz[3] = z0.w;
       zz[4] = z1.x; zz[5] = z1.y; zz[6] = z1.z; zz[7] = z1.w;
-      for (int i0 = 0; i0 < TP; i0 += RPP, i += RPP) {       // the same number of passes for every lane
-        uint4 nq, nk, o[4];
-        load_qk(i + RPP, nq, nk);
-        float zq = feature_rows(xq, xk, zz, o);
-        if (i < TP) {
-          *reinterpret_cast<uint4*>(sm + L.qh + i * QP + 16 * ch) = o[0];
-          *reinterpret_cast<uint4*>(sm + L.ql + i * QP + 16 * ch) = o[1];
-          *reinterpret_cast<uint4*>(sm + L.kh + i * QP + 16 * ch) = o[2];
-          *reinterpret_cast<uint4*>(sm + L.kl + i * QP + 16 * ch) = o[3];
-        }
+    }
+#pragma unroll 1
+    for (int i0 = 0; i0 < TP; i0 += PB * RPP) {
+      uint4 xq[PB], xk[PB];
 #pragma unroll
-        for (int off = 1; off < CH; off <<= 1) zq += __shfl_xor_sync(0xffffffffu, zq, off);
-        if (ch == 0 && i < TP) zqs[i] = zq;
-        xq = nq;
-        xk = nk;
+      for (int p = 0; p < PB; ++p) {
+        const int i = i0 + p * RPP + tid / CH;
+        xq[p] = xk[p] = zero4;
+        if (i < n) {
+          xq[p] = *reinterpret_cast<const uint4*>(qb + i * DK + 8 * ch);
+          xk[p] = *reinterpret_cast<const uint4*>(kb + i * DK + 8 * ch);
+        }
       }
-      for (; iv < TP; iv += RPV) {
-        xv[1] = iv + RPV < n ? *reinterpret_cast<const uint4*>(vb + (iv + RPV) * DV + 8 * chv) : zero4;
-        odd_values |= clear_nonfinite(xv[0]);
-        store_columns(sm + L.v + iv * VP, chv, xv[0]);
-        xv[0] = xv[1];
+#pragma unroll
+      for (int p = 0; p < PB; ++p) {
+        if (i0 + p * RPP >= TP) break;               // the same for all lanes
+        const int i = i0 + p * RPP + tid / CH;
+        if constexpr (kDelta) {
+          if (i < TP) {
+            *reinterpret_cast<uint4*>(sm + L.qh + i * QP + 16 * ch) = xq[p];
+            *reinterpret_cast<uint4*>(sm + L.kh + i * QP + 16 * ch) = xk[p];
+          }
+        } else {
+          uint4 o[4];
+          float zq = feature_rows(xq[p], xk[p], zz, o);
+          if (i < TP) {
+            *reinterpret_cast<uint4*>(sm + L.qh + i * QP + 16 * ch) = o[0];
+            *reinterpret_cast<uint4*>(sm + L.ql + i * QP + 16 * ch) = o[1];
+            *reinterpret_cast<uint4*>(sm + L.kh + i * QP + 16 * ch) = o[2];
+            *reinterpret_cast<uint4*>(sm + L.kl + i * QP + 16 * ch) = o[3];
+          }
+#pragma unroll
+          for (int off = 1; off < CH; off <<= 1) zq += __shfl_xor_sync(0xffffffffu, zq, off);
+          if (i < TP) zqs[i] = zq;                     // the same number from every lane of the row: no divergence
+        }
+      }
+    }
+    if constexpr (!kDelta) {
+#pragma unroll
+      for (int p = 0; p < PV; ++p) {
+        const int iv = tid / CHV + p * RPV;
+        if (iv < TP) {
+          odd_values |= clear_nonfinite(xv[p]);
+          store_columns(sm + L.v + iv * VP, chv, xv[p]);
+        }
       }
     }
   }
@@ -268,17 +278,25 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
       // lane: rows 16 mi + g (+ 8), columns 16 mj + 8 nj + 2t (+ 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = 16 * mi + g + 8 * e, dr = depth[row];
-        const unsigned long long m = mask[row];
+        const int r = g + 8 * e, row = 16 * mi + r, dr = depth[row];
+        const uint32_t m = (uint32_t)(mask[row] >> (16 * mj)) >> (2 * t);     // bits 0, 1, 8, 9: this lane's columns
         float sum = 0.f;
 #pragma unroll
         for (int nj = 0; nj < 2; ++nj) {
-          const int col = 16 * mj + 8 * nj + 2 * t;
-          const bool on0 = (m >> col) & 1, on1 = (m >> (col + 1)) & 1;
+          const int c = 8 * nj + 2 * t, col = 16 * mj + c;
+          const bool on0 = (m >> (8 * nj)) & 1, on1 = (m >> (8 * nj + 1)) & 1;
           float w0 = d[nj][2 * e], w1 = d[nj][2 * e + 1];
+          uint32_t hi, lo;
           if constexpr (kDelta) {
-            A[col * AP + row] = on0 && row != col ? d2[nj][2 * e] : 0.f;
-            A[(col + 1) * AP + row] = on1 && row != col + 1 ? d2[nj][2 * e + 1] : 0.f;
+            const float a0 = on0 && (mi != mj || r != c) ? d2[nj][2 * e] : 0.f;
+            const float a1 = on1 && (mi != mj || r != c + 1) ? d2[nj][2 * e + 1] : 0.f;
+            if (mi == mj) {
+              *reinterpret_cast<float2*>(tri + row * 16 + c) = make_float2(a0, a1);
+            } else {
+              split2(-a0, -a1, hi, lo);
+              *reinterpret_cast<uint32_t*>(sm + L.ah + row * WP + 2 * col) = hi;
+              *reinterpret_cast<uint32_t*>(sm + L.al + row * WP + 2 * col) = lo;
+            }
           } else {
             w0 += d2[nj][2 * e];
             w1 += d2[nj][2 * e + 1];
@@ -290,7 +308,6 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
           w0 = on0 ? w0 : 0.f;
           w1 = on1 ? w1 : 0.f;
           sum += w0 + w1;
-          uint32_t hi, lo;
           split2(w0, w1, hi, lo);
           *reinterpret_cast<uint32_t*>(sm + L.wh + row * WP + 2 * col) = hi;
           *reinterpret_cast<uint32_t*>(sm + L.wl + row * WP + 2 * col) = lo;
@@ -298,16 +315,14 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
         if constexpr (!kDelta) {
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (t == 0) den[mj * TP + row] = sum;
+          den[mj * TP + row] = sum;                // the same number from the row's four lanes
         }
       }
     }
   }
-  if (!kDelta) {                                   // (the delta rule's pairs and its read share nothing but q and k)
-    // the buffers were ordinary memory until here, the copies' next
-    if (L.overlay) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
-  }
+  // (overlay: the buffers were ordinary memory until here, the copies' next)
+  if (L.overlay) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
 
   // ---- read: D[c][i] = sum_r S[r][c] x_i[r], slab by slab
   float acc[NTM][4], acck[kDelta ? NTM : 1][4];
@@ -320,11 +335,18 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
     }
   const int c0 = 16 * warp + 2 * g;                // this lane's columns: c0, c0 + 1
   if (warp == NW) {
-    if (lane == 0) {
-      if (L.overlay) {
-        load_slab(0);
-        if (SLABS > 1) load_slab(1);
+    if (L.overlay && lane == 0) {
+      load_slab(0);
+      if (SLABS > 1) load_slab(1);
+    }
+    __syncwarp();
+    if constexpr (kDelta)
+      for (int x = lane; x < TP; x += 32) {        // 16 lanes per diagonal block
+        const int at16 = (x & ~15) * WP + 2 * (x & ~15);
+        invert_unit_triangle(tri + (x & ~15) * 16, x & 15, sm + L.ah + at16, sm + L.al + at16, WP);
       }
+    __syncwarp();
+    if (lane == 0) {
       for (int s = 2; s < SLABS; ++s) {
         if (!sm100::mbar_drain(empty + (s & 1), ((s >> 1) - 1) & 1, kWaitNs)) atomicExch(status, (int)LA_ERR_TIMEOUT);
         load_slab(s);
@@ -392,85 +414,39 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
   }
   __syncthreads();
 
+  uint32_t uh[kDelta ? NTM / 2 : 1][4], ul[kDelta ? NTM / 2 : 1][4];     // u as the A operand, block by block
   if constexpr (kDelta) {
-    // ---- R = v - S^T k where the slabs were
+    int odd_u = 0;
     if (warp < NW) {
+      const uint32_t at = base + L.ah + lrow * WP + lcol;
 #pragma unroll
-      for (int nt = 0; nt < NTM; ++nt)
-        if (nt < tiles) {
+      for (int ib = 0; ib < NTM / 2; ++ib)
+        if (ib < blocks) {
+          // R = v - S^T k, less the earlier blocks' part, through the triangle
+          float r[2][4], u[2][4] = {};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = 8 * nt + 2 * t + e;
-            const uint32_t x = j < n ? *reinterpret_cast<const uint32_t*>(vb + j * DV + c0) : 0u;
-            *reinterpret_cast<float2*>(R + j * RP + c0) =
-                make_float2(low_half(x) - acck[nt][e], high_half(x) - acck[nt][2 + e]);
-          }
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = 16 * ib + 8 * nt + 2 * t + e;
+              const uint32_t x = j < n ? *reinterpret_cast<const uint32_t*>(vb + j * DV + c0) : 0u;
+              r[nt][e] = low_half(x) - acck[2 * ib + nt][e];
+              r[nt][2 + e] = high_half(x) - acck[2 * ib + nt][2 + e];
+            }
+#pragma unroll
+          for (int jb = 0; jb < ib; ++jb)
+            mma_block(r[0], r[1], uh[jb], ul[jb], at + 16 * ib * WP + 32 * jb, at + (L.al - L.ah) + 16 * ib * WP + 32 * jb);
+          uint32_t rh[4], rl[4];
+          as_operand(r[0], r[1], rh, rl);
+          mma_block(u[0], u[1], rh, rl, at + 16 * ib * WP + 32 * ib, at + (L.al - L.ah) + 16 * ib * WP + 32 * ib);
+          odd_u |= any_nonfinite(u[0]) || any_nonfinite(u[1]);
+          as_operand(u[0], u[1], uh[ib], ul[ib]);
         }
     }
-    __syncthreads();
-    // ---- u_j = R_j - sum_{l on j's path} (k_j.k_l) u_l: two lanes per
-    // column, blocks of 8 nodes: the earlier nodes' part first (each lane
-    // every other node, 8 sums at a time), then the block's own triangle.
-    // `off`: earlier nodes whose u is not finite in this column; while there
-    // is none, the zeros of A leave the other paths out.
-    if (warp < NW) {
-      const int c = tid >> 1, half = tid & 1;
-      unsigned long long off = 0ull;
-      for (int j0 = 0; j0 < TP; j0 += 8) {
-        float u[8];
-        if (j0 < n) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] = half == 0 ? R[(j0 + e) * RP + c] : 0.f;
-#pragma unroll 2
-          for (int l = half; l < j0; l += 2) {
-            const float ul = R[l * RP + c];
-            const float4 a0 = *reinterpret_cast<const float4*>(A + l * AP + j0);
-            const float4 a1 = *reinterpret_cast<const float4*>(A + l * AP + j0 + 4);
-            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            if (!((off >> l) & 1)) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) u[e] = fmaf(-av[e], ul, u[e]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if ((mask[j0 + e] >> l) & 1) u[e] = fmaf(-av[e], ul, u[e]);
-            }
-          }
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] += __shfl_xor_sync(0xffffffffu, u[e], 1);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-#pragma unroll
-            for (int l = 0; l < e; ++l) {
-              const float x = fmaf(-A[(j0 + l) * AP + j0 + e], u[l], u[e]);
-              u[e] = (mask[j0 + e] >> (j0 + l)) & 1 ? x : u[e];
-            }
-            if (j0 + e >= n) u[e] = 0.f;
-            if (nonfinite(u[e])) off |= 1ull << (j0 + e);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] = 0.f;
-        }
-        const int at = (c >> 4) * 32 + (c & 1) * 16 + ((c & 15) >> 1) * 2;   // even columns of a block first
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if ((e & 1) == half) {
-            const int j = j0 + e;
-            R[j * RP + c] = u[e];
-            const float x = nonfinite(u[e]) ? 0.f : u[e];
-            const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-            *reinterpret_cast<__nv_bfloat16*>(sm + L.v + j * VP + at) = hi;
-            *reinterpret_cast<__nv_bfloat16*>(sm + L.vl + j * VP + at) = __float2bfloat16_rn(x - __bfloat162float(hi));
-          }
-        __syncwarp();
-      }
-      if (off & 0xffffffffull) atomicOr(bad, (unsigned int)off);
-      if (off >> 32) atomicOr(bad + 1, (unsigned int)(off >> 32));
+    if (__syncthreads_or(odd_u)) {
+      delta_tree_by_paths<DK, DV>(S + bh * (long long)(DK * DV), qb, kb, vb, ob, mask, n, reinterpret_cast<float*>(sm));
+      return;
     }
-    __syncthreads();
-    spoilt = (unsigned long long)bad[0] | ((unsigned long long)bad[1] << 32);
   }
   if (warp >= NW) return;
 
@@ -489,67 +465,65 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
 
   // ---- path: D[c][i] += sum_j V[j][c] W[i][j], j in steps of 16
   {
-    const int mat = lane >> 3, rr = lane & 7;
-    const uint32_t va = base + L.v + (rr + (mat >> 1) * 8) * VP + 32 * warp + (mat & 1) * 16;
+    const uint32_t va = base + L.v + ((lane & 7) + (lane >> 4) * 8) * VP + 32 * warp + ((lane >> 3) & 1) * 16;
     const uint32_t wa = base + L.wh + lrow * WP + lcol;
 #pragma unroll
     for (int js = 0; js < NTM / 2; ++js)
       if (js < blocks) {
-        uint32_t a[4], al[4];
-        ldmatrix4t(a, va + js * 16 * VP);
-        if constexpr (kDelta) ldmatrix4t(al, va + (L.vl - L.v) + js * 16 * VP);
+        uint32_t a[4];
+        if constexpr (!kDelta) ldmatrix4t(a, va + js * 16 * VP);
 #pragma unroll
         for (int ib = js; ib < NTM / 2; ++ib)
           if (ib < blocks) {
-            uint32_t wh[4], wl[4];
-            ldmatrix4(wh, wa + ib * 16 * WP + 32 * js);
-            ldmatrix4(wl, wa + (L.wl - L.wh) + ib * 16 * WP + 32 * js);
-            mma(acc[2 * ib], a, wh[0], wh[2]);
-            mma(acc[2 * ib + 1], a, wh[1], wh[3]);
-            mma(acc[2 * ib], a, wl[0], wl[2]);
-            mma(acc[2 * ib + 1], a, wl[1], wl[3]);
+            const uint32_t w = wa + ib * 16 * WP + 32 * js;
             if constexpr (kDelta) {
-              mma(acc[2 * ib], al, wh[0], wh[2]);
-              mma(acc[2 * ib + 1], al, wh[1], wh[3]);
+              mma_block(acc[2 * ib], acc[2 * ib + 1], uh[js], ul[js], w, w + (L.wl - L.wh));
+            } else {
+              uint32_t wh[4], wl[4];
+              ldmatrix4(wh, w);
+              ldmatrix4(wl, w + (L.wl - L.wh));
+              mma(acc[2 * ib], a, wh[0], wh[2]);
+              mma(acc[2 * ib + 1], a, wh[1], wh[3]);
+              mma(acc[2 * ib], a, wl[0], wl[2]);
+              mma(acc[2 * ib + 1], a, wl[1], wl[3]);
             }
           }
       }
   }
 
   // ---- out: lane holds nodes 8 nt + 2t (+ 1), columns c0, c0 + 1
+  if (!kDelta && spoilt != 0ull) {
+    // the values left out of v, for the nodes below them
 #pragma unroll
-  for (int nt = 0; nt < NTM; ++nt)
-    if (nt < tiles) {
+    for (int nt = 0; nt < NTM; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int node = 8 * nt + 2 * t + e;
         if (node >= n) continue;
-        float o0 = acc[nt][e], o1 = acc[nt][2 + e];
-        if (spoilt != 0ull) {
-          for (unsigned long long m = mask[node] & spoilt; m != 0ull; m &= m - 1) {
-            const int j = __ffsll((long long)m) - 1;
-            float x0, x1;
-            if constexpr (kDelta) {
-              x0 = R[j * RP + c0];
-              x1 = R[j * RP + c0 + 1];
-            } else {
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(vb + j * DV + c0);
-              x0 = low_half(x);
-              x1 = high_half(x);
-            }
-            const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L.wh + node * WP + 2 * j)) +
-                            __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L.wl + node * WP + 2 * j));
-            if (nonfinite(x0)) o0 = fmaf(w, x0, o0);
-            if (nonfinite(x1)) o1 = fmaf(w, x1, o1);
-          }
+        for (unsigned long long m = mask[node] & spoilt; m != 0ull; m &= m - 1) {
+          const int j = __ffsll((long long)m) - 1;
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(vb + j * DV + c0);
+          const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L.wh + node * WP + 2 * j)) +
+                          __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + L.wl + node * WP + 2 * j));
+          if (nonfinite(low_half(x))) acc[nt][e] = fmaf(w, low_half(x), acc[nt][e]);
+          if (nonfinite(high_half(x))) acc[nt][2 + e] = fmaf(w, high_half(x), acc[nt][2 + e]);
         }
-        if constexpr (!kDelta) {
-          o0 *= rden[node];
-          o1 *= rden[node];
-        }
-        *reinterpret_cast<uint32_t*>(ob + (long long)node * DV + c0) = pack2(o0, o1);
       }
-    }
+  }
+  {
+    __nv_bfloat16* o = ob + (2 * t) * DV + c0;
+    const float* rd = rden + 2 * t;
+#pragma unroll
+    for (int nt = 0; nt < NTM; ++nt)
+      if (nt < tiles) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float r = kDelta ? 1.f : rd[8 * nt + e];
+          const uint32_t x = pack2(acc[nt][e] * r, acc[nt][2 + e] * r);
+          if (8 * nt + 2 * t + e < n) *reinterpret_cast<uint32_t*>(o + (8 * nt + e) * DV) = x;
+        }
+      }
+  }
 }
 
 template <int DK, int DV, bool kDelta>
@@ -558,6 +532,9 @@ cudaError_t launch(const TreeArgs& a) {
   constexpr Sh most(TM), middle(48);
   // two CTAs per SM (228 KiB, 1 KiB of it taken by each CTA)
   static_assert(most.total + 1024 <= 116736 && middle.total + 1024 <= 116736, "shared memory of two CTAs");
+  static_assert(!kDelta || (TM * (2 * (TM + 1) + DV) * 4 <= most.mask && 32 * (2 * 33 + DV) * 4 <= Sh(32).mask &&
+                            48 * (2 * 49 + DV) * 4 <= middle.mask),
+                "room for delta_tree_by_paths");
   static_assert(most.ring % 1024 == 0, "the swizzle goes by address bits");
   const Sh L((a.T + 15) & ~15);
   auto kern = tree_wide_kernel<DK, DV, kDelta>;
