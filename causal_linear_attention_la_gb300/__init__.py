@@ -756,8 +756,8 @@ def verify_chain(target, draft, tokens, uniform, count=None):
     code = _dtype_code(target)
     _need_like(dev, ("target", target, target.dtype, (B, T + 1, V)), ("draft", draft, target.dtype, (B, T, V)),
                ("tokens", tokens, i32, (B, T)), ("uniform", uniform, torch.float32, (B, T + 1)), ("count", count, i32, (B,)))
-    got = torch.empty((2, B), dtype=i32, device=target.device)
-    accepted, nxt = got.unbind()
+    accepted = torch.empty((B,), dtype=i32, device=target.device)
+    nxt = torch.empty((B,), dtype=i32, device=target.device)
     _on(dev, la_verify_chain, target.data_ptr(), draft.data_ptr(), tokens.data_ptr(), _ptr(count),
         uniform.data_ptr(), accepted.data_ptr(), nxt.data_ptr(), B, T, V, code)
     return accepted, nxt
@@ -775,7 +775,8 @@ def verify_tree(target, tokens, parent, uniform, count=None):
     _need_like(dev, ("target", target, target.dtype, (B, T + 1, V)), ("tokens", tokens, i32, (B, T)),
                ("parent", parent, i32, (B, T)), ("uniform", uniform, torch.float32, (B, T + 1)), ("count", count, i32, (B,)))
     path = torch.empty((B, T), dtype=i32, device=target.device)
-    accepted, nxt = torch.empty((2, B), dtype=i32, device=target.device).unbind()
+    accepted = torch.empty((B,), dtype=i32, device=target.device)
+    nxt = torch.empty((B,), dtype=i32, device=target.device)
     _on(dev, la_verify_tree, target.data_ptr(), tokens.data_ptr(), parent.data_ptr(), _ptr(count),
         uniform.data_ptr(), path.data_ptr(), accepted.data_ptr(), nxt.data_ptr(), B, T, V, code)
     return path, accepted, nxt

@@ -412,6 +412,22 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
       if (lane == 0 && s + 2 < SLABS) sm100::mbar_arrive(empty + (s & 1));
     }
   }
+  if constexpr (kDelta) {
+    // R = v - S^T k, all of this lane's values of v in flight at once
+    if (warp < NW) {
+#pragma unroll
+      for (int nt = 0; nt < NTM; ++nt)
+        if (nt < 2 * blocks) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = 8 * nt + 2 * t + e;
+            const uint32_t x = j < n ? *reinterpret_cast<const uint32_t*>(vb + j * DV + c0) : 0u;
+            acck[nt][e] = low_half(x) - acck[nt][e];
+            acck[nt][2 + e] = high_half(x) - acck[nt][2 + e];
+          }
+        }
+    }
+  }
   __syncthreads();
 
   uint32_t uh[kDelta ? NTM / 2 : 1][4], ul[kDelta ? NTM / 2 : 1][4];     // u as the A operand, block by block
@@ -422,22 +438,14 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
 #pragma unroll
       for (int ib = 0; ib < NTM / 2; ++ib)
         if (ib < blocks) {
-          // R = v - S^T k, less the earlier blocks' part, through the triangle
-          float r[2][4], u[2][4] = {};
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = 16 * ib + 8 * nt + 2 * t + e;
-              const uint32_t x = j < n ? *reinterpret_cast<const uint32_t*>(vb + j * DV + c0) : 0u;
-              r[nt][e] = low_half(x) - acck[2 * ib + nt][e];
-              r[nt][2 + e] = high_half(x) - acck[2 * ib + nt][2 + e];
-            }
+          // R less the earlier blocks' part, through the triangle
+          float (&r0)[4] = acck[2 * ib], (&r1)[4] = acck[2 * ib + 1];
+          float u[2][4] = {};
 #pragma unroll
           for (int jb = 0; jb < ib; ++jb)
-            mma_block(r[0], r[1], uh[jb], ul[jb], at + 16 * ib * WP + 32 * jb, at + (L.al - L.ah) + 16 * ib * WP + 32 * jb);
+            mma_block(r0, r1, uh[jb], ul[jb], at + 16 * ib * WP + 32 * jb, at + (L.al - L.ah) + 16 * ib * WP + 32 * jb);
           uint32_t rh[4], rl[4];
-          as_operand(r[0], r[1], rh, rl);
+          as_operand(r0, r1, rh, rl);
           mma_block(u[0], u[1], rh, rl, at + 16 * ib * WP + 32 * ib, at + (L.al - L.ah) + 16 * ib * WP + 32 * ib);
           odd_u |= any_nonfinite(u[0]) || any_nonfinite(u[1]);
           as_operand(u[0], u[1], uh[ib], ul[ib]);
