@@ -22,9 +22,11 @@
 //
 // One thread-block cluster per sequence: each CTA takes a contiguous part of
 // the vocabulary, each warp a contiguous part of that, so that the joined
-// sums are prefix sums in token order. The CTAs exchange their totals through
-// distributed shared memory; the one whose part holds the answer finds the
-// warp's part, splits that over its warps again and scans the last piece.
+// sums are prefix sums in token order. Every warp sends its sum to all CTAs
+// (distributed shared memory), every warp finds the part that holds the answer
+// by one scan over all of them; the CTA that has it splits it over its warps
+// again and scans the last piece. (Sums joined per CTA first, and added up one
+// after the other, took as long as the rows: 31 us for the trees below.)
 // Bound by latency up to a few sequences (row, exchange, search one after the
 // other) and by HBM beyond. Barriers of the cluster stand where every CTA comes by:
 // what they depend on is exchanged, not worked out by each CTA for itself.
@@ -61,15 +63,12 @@ __device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
                : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void peer_store(uint32_t addr, float x) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
-}
 __device__ __forceinline__ void peer_store(uint32_t addr, int x) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 
 // A number as the sum of two fp32 words, |l| at most half a step of h.
-struct Pair {
+struct __align__(8) Pair {
   float h, l;
 };
 
@@ -89,6 +88,23 @@ __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
   float s, e;
   two_sum(a.h, b.h, s, e);
   return normalised(s, __fadd_rn(e, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, Pair x) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x.h), "f"(x.l) : "memory");
+}
+__device__ __forceinline__ Pair from_lane(Pair x, int lane) {
+  return {__shfl_sync(0xffffffffu, x.h, lane), __shfl_sync(0xffffffffu, x.l, lane)};
+}
+// Sums over lanes 0 .. this one, for the first N lanes.
+template <int N>
+__device__ __forceinline__ Pair prefix(Pair x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < N; o <<= 1) {
+    const Pair y = {__shfl_up_sync(0xffffffffu, x.h, o), __shfl_up_sync(0xffffffffu, x.l, o)};
+    if (lane >= o) x = x + y;
+  }
+  return x;
 }
 __device__ __forceinline__ bool operator>(Pair a, Pair b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
 __device__ __forceinline__ Pair operator*(float u, Pair a) {
@@ -125,9 +141,20 @@ __device__ __forceinline__ Pair weight(float p, float q) {
   return w;
 }
 
+// Where a draw with u ends up: the part (of nc * VW) that holds the answer, the
+// sum of the parts before it, what the draw has to pass; `end`: rounding left
+// no part, it is the last token with a weight in the last part that has one.
+struct Found {
+  Pair total, want, before;
+  int part;
+  bool end;
+};
+
 struct VerifyShared {
-  Pair warp_sum[VW], sub_sum[VW];
-  Pair cta_sum[kMaxCluster];         // every CTA's total, in every CTA
+  Pair sums[kMaxCluster * VW];       // every warp's total, in every CTA of the cluster
+  Pair sub_sum[VW];
+  Found found_part;
+  int piece;
   int answer[2];                     // token drawn, child entered
   int found;
   int par[kTreeMax], tok[kTreeMax];
@@ -140,6 +167,7 @@ template <>
 struct Vec<float> {
   static constexpr int N = 4;
   float4 v;
+  __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
   __device__ __forceinline__ float get(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 };
@@ -147,6 +175,7 @@ template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
   uint4 v;
+  __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
@@ -154,12 +183,12 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// The tokens of warp `w` of CTA `rank`, out of nc * VW parts in order: whole
-// vector loads of a warp.
+// The tokens of warp `w` of CTA `rank`, out of nc * VW parts in order, each a
+// multiple of 32.
 struct Part {
   int w0, w1;
   __device__ Part(int V, int rank, int nc, int w) {
-    const int per = ((V + nc * VW - 1) / (nc * VW) + 255) & ~255;
+    const int per = ((V + nc * VW - 1) / (nc * VW) + 31) & ~31;
     const long long lo = (long long)(rank * VW + w) * per;
     w0 = (int)min(lo, (long long)V);
     w1 = (int)min(lo + per, (long long)V);
@@ -177,131 +206,186 @@ __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
     two_sum(hi, w.h, hi, r);
     lo += w.l + r;
   };
+  // (batches of loads under their own bounds: a loop's remainder would wait for
+  // every load by itself)
   constexpr int N = Vec<T>::N;
   if (vec) {
-    if (q != nullptr) {
-#pragma unroll 4
-      for (int t = t0 + N * lane; t < t1; t += 32 * N) {
-        Vec<T> x, y;
-        x.load(p + t);
-        y.load(q + t);
+    constexpr int U = 4;
+    for (int tb = t0 + N * lane; tb < t1; tb += U * 32 * N) {
+      Vec<T> x[U], y[U];
 #pragma unroll
-        for (int i = 0; i < N; ++i) add(weight(x.get(i), y.get(i)));
+      for (int i = 0; i < U; ++i) {
+        const int t = tb + i * 32 * N;
+        x[i].clear();
+        y[i].clear();
+        if (t < t1) {
+          x[i].load(p + t);
+          if (q != nullptr) y[i].load(q + t);
+        }
       }
-    } else {
-#pragma unroll 4
-      for (int t = t0 + N * lane; t < t1; t += 32 * N) {
-        Vec<T> x;
-        x.load(p + t);
 #pragma unroll
-        for (int i = 0; i < N; ++i) add(weight(x.get(i)));
-      }
+      for (int i = 0; i < U; ++i)
+        if (tb + i * 32 * N < t1) {
+          if (q != nullptr) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) add(weight(x[i].get(e), y[i].get(e)));
+          } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) add(weight(x[i].get(e)));
+          }
+        }
     }
-  } else if (q != nullptr) {
-#pragma unroll 8
-    for (int t = t0 + lane; t < t1; t += 32) add(weight(to_f32<T>(p[t]), to_f32<T>(q[t])));
   } else {
-#pragma unroll 8
-    for (int t = t0 + lane; t < t1; t += 32) add(weight(to_f32<T>(p[t])));
+    constexpr int U = 8;
+    for (int tb = t0 + lane; tb < t1; tb += U * 32) {
+      float x[U], y[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int t = tb + i * 32;
+        x[i] = y[i] = 0.f;
+        if (t < t1) {
+          x[i] = to_f32<T>(p[t]);
+          if (q != nullptr) y[i] = to_f32<T>(q[t]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) add(q != nullptr ? weight(x[i], y[i]) : weight(x[i]));
+    }
   }
   return warp_total(normalised(hi, lo));
 }
 
-// The row's total, the same in every CTA: the parts' sums, this CTA's own sent
-// to every CTA of the cluster (one cluster barrier).
+// The sums of all warps' parts of a row, in every CTA (one cluster barrier).
 template <typename T>
-__device__ Pair row_total(const T* p, const T* q, int V, bool vec, int rank, int nc, VerifyShared& sh) {
+__device__ void row_sums(const T* p, const T* q, int V, bool vec, int rank, int nc, VerifyShared& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Part part(V, rank, nc, warp);
   const Pair x = span_total(p, q, part.w0, part.w1, vec);
-  if (lane == 0) sh.warp_sum[warp] = x;
-  __syncthreads();
-  if (threadIdx.x < nc) {
-    Pair t = sh.warp_sum[0];
-    for (int w = 1; w < VW; ++w) t = t + sh.warp_sum[w];
-    const uint32_t to = peer(&sh.cta_sum[rank], threadIdx.x);
-    peer_store(to, t.h);
-    peer_store(to + 4, t.l);
-  }
+  if (lane < nc) peer_store(peer(&sh.sums[rank * VW + warp], lane), x);
   __syncwarp();
   cluster_sync();
-  Pair total = sh.cta_sum[0];
-  for (int r = 1; r < nc; ++r) total = total + sh.cta_sum[r];
-  return total;
 }
 
-// The first of n sums whose prefix (from `before`) passes `want`, `before`
-// then being the prefix in front of it; the last positive one (and `end`)
-// where none does, as rounding may have it.
-__device__ __forceinline__ int pass(const Pair* sums, int n, Pair want, Pair& before, bool& end) {
-  int last = 0;
-  Pair sum = before;
-  for (int i = 0; i < n; ++i) {
-    const Pair c = sums[i];
-    if (!(c.h > 0.f)) continue;
+// By one warp, from row_sums: a lane takes nc / 2 sums in a row (one of 16 for
+// a single CTA).
+__device__ __forceinline__ Found find_part_warp(const VerifyShared& sh, int nc, float u) {
+  const int lane = threadIdx.x & 31, per = nc > 1 ? nc * VW / 32 : 1;
+  const Pair* mine = sh.sums + lane * per;
+  const bool has = lane * per < nc * VW;
+  Pair sum = {0.f, 0.f};
+  for (int i = 0; i < per; ++i)
+    if (has) sum = sum + mine[i];
+  const Pair upto = prefix<32>(sum);
+  Found f;
+  f.total = from_lane(upto, 31);
+  f.want = u * f.total;
+  const bool some = sum.h > 0.f;
+  const unsigned past = __ballot_sync(0xffffffffu, some && upto > f.want);
+  const unsigned any = __ballot_sync(0xffffffffu, some);
+  f.end = past == 0u;
+  const int at = f.end ? (any != 0u ? 31 - __clz(any) : 0) : __ffs(past) - 1;
+  const Pair front = from_lane(upto, at > 0 ? at - 1 : 0);
+  f.before = at > 0 ? front : Pair{0.f, 0.f};
+  // among that lane's sums
+  const Pair* theirs = sh.sums + at * per;
+  int last = 0, hit = -1;
+  sum = f.before;
+  for (int i = 0; i < per && hit < 0; ++i) {
+    const Pair x = theirs[i];
+    if (!(x.h > 0.f)) continue;
     last = i;
-    const Pair next = sum + c;
-    if (!end && next > want) {
-      before = sum;
-      return i;
+    const Pair next = sum + x;
+    if (!f.end && next > f.want) {
+      hit = i;
+      f.before = sum;
     }
     sum = next;
   }
-  end = true;
-  return last;
+  if (hit < 0) f.end = true;
+  f.part = at * per + (hit < 0 ? last : hit);
+  return f;
 }
 
-// The token drawn with u from a row whose row_total is `total` > 0: returned
-// by every thread of the CTA whose part holds it, -1 elsewhere.
-template <typename T>
-__device__ int draw(const T* p, const T* q, int V, bool vec, float u, Pair total, int rank, int nc, VerifyShared& sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Pair want = u * total;
-  Pair before = {0.f, 0.f};
-  bool end = false;
-  if (pass(sh.cta_sum, nc, want, before, end) != rank) return -1;
-  const int w = pass(sh.warp_sum, VW, want, before, end);
-  // that warp's part again, over all warps
-  const Part part(V, rank, nc, w);
-  const int sub = ((part.w1 - part.w0 + VW - 1) / VW + 31) & ~31;
-  {
-    const int t0 = min(part.w0 + warp * sub, part.w1);
-    const Pair x = span_total(p, q, t0, min(t0 + sub, part.w1), false);
-    if (lane == 0) sh.sub_sum[warp] = x;
+// By the CTA: one warp searches (the pair arithmetic of sixteen would queue up).
+__device__ __forceinline__ Found find_part(VerifyShared& sh, int nc, float u) {
+  if (threadIdx.x < 32) {
+    const Found f = find_part_warp(sh, nc, u);
+    if (threadIdx.x == 0) sh.found_part = f;
   }
   __syncthreads();
-  const int m = pass(sh.sub_sum, VW, want, before, end);
-  if (warp == m) {
-    const int t0 = part.w0 + m * sub, t1 = min(t0 + sub, part.w1);
+  return sh.found_part;
+}
+
+// The token of a draw whose part this CTA has: that part again, over all warps.
+// Returned to every thread.
+template <typename T>
+__device__ int draw(const T* p, const T* q, int V, const Found& f, int rank, int nc, VerifyShared& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Part part(V, rank, nc, f.part % VW);
+  const int sub = ((part.w1 - part.w0 + VW - 1) / VW + 31) & ~31;
+  const int t0 = min(part.w0 + warp * sub, part.w1), t1 = min(t0 + sub, part.w1);
+  auto token_weight = [&](int t) {
+    if (t >= t1) return Pair{0.f, 0.f};
+    const float a = to_f32<T>(p[t]);
+    return q != nullptr ? weight(a, to_f32<T>(q[t])) : weight(a);
+  };
+  // (a piece of 32 tokens is scanned at once, a longer one summed first)
+  Pair x = {0.f, 0.f}, upto = {0.f, 0.f}, sum;
+  if (sub == 32) {
+    x = token_weight(t0 + lane);
+    upto = prefix<32>(x);
+    sum = from_lane(upto, 31);
+  } else {
+    sum = span_total(p, q, t0, t1, false);
+  }
+  if (lane == 0) sh.sub_sum[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    // the piece, and the sum in front of it
+    const Pair c = lane < VW ? sh.sub_sum[lane] : Pair{0.f, 0.f};
+    const Pair pieces = f.before + prefix<VW>(c);
+    const bool some = lane < VW && c.h > 0.f;
+    const unsigned past = __ballot_sync(0xffffffffu, some && pieces > f.want);
+    const unsigned any = __ballot_sync(0xffffffffu, some);
+    const bool end = f.end || past == 0u;
+    const int m = end ? (any != 0u ? 31 - __clz(any) : 0) : __ffs(past) - 1;
+    const Pair front = from_lane(pieces, m > 0 ? m - 1 : 0);
+    if (lane == 0) {
+      sh.piece = m;
+      sh.found_part.before = m > 0 ? front : f.before;
+      sh.found_part.end = end;
+    }
+  }
+  __syncthreads();
+  if (warp == sh.piece) {
+    Pair before = sh.found_part.before;
+    const bool end = sh.found_part.end;
     int pick = -1;
     for (int t = t0; t < t1; t += 32) {
-      Pair x = {0.f, 0.f};
-      if (t + lane < t1) {
-        const float a = to_f32<T>(p[t + lane]);
-        x = q != nullptr ? weight(a, to_f32<T>(q[t + lane])) : weight(a);
+      if (sub != 32) {
+        x = token_weight(t + lane);
+        upto = prefix<32>(x);
       }
       const bool some = x.h > 0.f;
-      const unsigned any = __ballot_sync(0xffffffffu, some);
-      if (any == 0u) continue;
-      pick = t + 31 - __clz(any);
+      const unsigned weighed = __ballot_sync(0xffffffffu, some);
+      if (weighed == 0u) continue;
+      pick = t + 31 - __clz(weighed);
       if (end) continue;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const Pair y = {__shfl_up_sync(0xffffffffu, x.h, o), __shfl_up_sync(0xffffffffu, x.l, o)};
-        if (lane >= o) x = x + y;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, some && before + x > want);
-      if (past != 0u) {
-        pick = t + __ffs(past) - 1;
+      const unsigned hit = __ballot_sync(0xffffffffu, some && before + upto > f.want);
+      if (hit != 0u) {
+        pick = t + __ffs(hit) - 1;
         break;
       }
-      before = before + Pair{__shfl_sync(0xffffffffu, x.h, 31), __shfl_sync(0xffffffffu, x.l, 31)};
+      before = before + from_lane(upto, 31);
     }
     if (lane == 0) sh.found = pick;
   }
   __syncthreads();
   return sh.found;
 }
+
+// A total that can be drawn from (an infinite weight makes it no number).
+__device__ __forceinline__ bool drawable(Pair total) { return total.h > 0.f && total.h <= 3.4e38f; }
 
 template <typename T>
 __global__ void __launch_bounds__(VT)
@@ -331,16 +415,17 @@ chain_kernel(const T* __restrict__ target, const T* __restrict__ draft, const in
   const T* p = pb + (long long)n * V;
   const T* q = n < all ? qb + (long long)n * V : nullptr;
   cluster_wait();
-  Pair total = row_total(p, q, V, vec, rank, nc, sh);
-  if (!(total.h > 0.f)) {
+  row_sums(p, q, V, vec, rank, nc, sh);
+  Found f = find_part(sh, nc, u);
+  if (!(f.total.h > 0.f)) {
     // nothing left to draw from (p <= q everywhere): from p itself
-    cluster_sync();                            // the totals have been read
+    cluster_sync();                            // the sums have been read
     q = nullptr;
-    total = row_total(p, q, V, vec, rank, nc, sh);
+    row_sums(p, q, V, vec, rank, nc, sh);
+    f = find_part(sh, nc, u);
   }
-  // (a row with an infinite weight has a total that is no number)
-  const bool some = total.h > 0.f && total.h <= 3.4e38f;
-  const int t = some ? draw(p, q, V, vec, u, total, rank, nc, sh) : -1;
+  const bool some = drawable(f.total);
+  const int t = some && f.part / VW == rank ? draw(p, q, V, f, rank, nc, sh) : -1;
   if (threadIdx.x == 0) {
     if (rank == 0) accepted[b] = n;
     if (t >= 0 || (rank == 0 && !some)) next[b] = t;
@@ -368,11 +453,12 @@ tree_verify_kernel(const T* __restrict__ target, const int* __restrict__ tokens,
   for (int step = 0; step <= ntok; ++step) {
     const T* p = pb + (long long)(at + 1) * V;
     const float u = uniform[(long long)b * (ntok + 1) + at + 1];
-    const Pair total = row_total<T>(p, nullptr, V, vec, rank, nc, sh);
+    row_sums<T>(p, nullptr, V, vec, rank, nc, sh);
+    const Found f = find_part(sh, nc, u);
     token = -1;
     int child = -1;
-    if (total.h > 0.f && total.h <= 3.4e38f) {
-      const int t = draw<T>(p, nullptr, V, vec, u, total, rank, nc, sh);
+    if (drawable(f.total)) {
+      const int t = f.part / VW == rank ? draw<T>(p, nullptr, V, f, rank, nc, sh) : -1;
       if (t >= 0 && threadIdx.x < 32) {
         // the first child that holds the token
         int hit = -1;
@@ -405,11 +491,13 @@ tree_verify_kernel(const T* __restrict__ target, const int* __restrict__ tokens,
   }
 }
 
-// CTAs per sequence. One CTA goes through about 4096 tokens before its joins
-// cost less than its sums; more than eight would need the non-portable size.
-int cluster_size(int V) {
+// CTAs per sequence: as many as keep 2048 tokens each and two CTAs per SM at
+// most (64 chains over 131072 fp32 tokens, rows in L2: 8 CTAs 26 us, 4 20, 2 24,
+// 1 36; 32 trees over 50021 bf16 tokens: 8 33 us, 4 32, 2 39, 1 52). More than
+// eight would need the non-portable cluster size.
+int cluster_size(int B, int V) {
   int nc = 1;
-  while (nc < kMaxCluster && V > 4096 * nc) nc *= 2;
+  while (nc < kMaxCluster && V > 2048 * nc && (long long)B * nc * 2 <= 2 * kSlots) nc *= 2;
   return nc;
 }
 
@@ -430,7 +518,7 @@ cudaError_t launch_cluster(void (*kern)(Params...), int B, int nc, cudaStream_t 
 
 template <typename T>
 cudaError_t launch(const VerifyArgs& a) {
-  const int nc = cluster_size(a.V);
+  const int nc = cluster_size(a.B, a.V);
   const bool vec = a.V % Vec<T>::N == 0;           // rows on 16-byte boundaries
   const T* p = (const T*)a.target;
   const cudaError_t e =
