@@ -16,9 +16,10 @@
 //
 // One CTA per (batch, head). The state is read once, straight into registers
 // (thread (rg, cg): E rows, four columns, all loads in flight together); the
-// nodes pass by it in groups of NB, the row groups' partial sums meet in
-// shared memory. The pair products and the sums over the path are register
-// tiles of 4 x 4 from shared memory. Everything is fp32.
+// nodes pass by it in groups of NB, the row groups' partial sums meet by
+// shuffles within a warp and then in shared memory. The pair products and the
+// sums over the path are register tiles from shared memory. Everything is
+// fp32; small trees are bound by the chain of these steps.
 #include "la_tree.cuh"
 
 namespace la {
@@ -31,7 +32,7 @@ struct TreeShape {
   static constexpr int NT = (CG * DK) < 256 ? (CG * DK) : 256;   // threads
   static constexpr int RG = NT / CG;                             // row groups
   static constexpr int E = DK / RG;                              // state rows per thread
-  static constexpr int NB = 8;                                   // nodes per group
+  static constexpr int NW = NT / 32;                             // warps: row groups after a warp's own have met
   static constexpr int QP = DK + 4;                              // pitch of q and k rows (bank-conflict free)
 };
 
@@ -39,7 +40,9 @@ struct TreeShape {
 template <int DK, int DV, bool kDelta>
 struct TreeSmem {
   int TP, WP, q, k, v, w, w2, qs, part, z, den, pw, depth, mask, up, total;
-  __host__ __device__ explicit TreeSmem(int T) {
+  static constexpr int NB = kDelta ? 8 : 16;         // nodes per group (the delta rule's layout is the larger)
+  __host__ __device__ constexpr explicit TreeSmem(int T)
+      : TP(0), WP(0), q(0), k(0), v(0), w(0), w2(0), qs(0), part(0), z(0), den(0), pw(0), depth(0), mask(0), up(0), total(0) {
     using Sh = TreeShape<DK, DV>;
     TP = (T + 3) & ~3;
     WP = TP + 4;
@@ -50,7 +53,7 @@ struct TreeSmem {
     w2 = w + TP * WP;
     qs = w2 + (kDelta ? TP * WP : 0);
     part = qs + TP * DV;
-    z = part + Sh::NB * Sh::RG * DV;
+    z = part + NB * Sh::NW * DV;
     den = z + DK;
     pw = den + TP;
     depth = pw + kTreeMax + 4;
@@ -74,33 +77,45 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 x
   *reinterpret_cast<uint2*>(p) = u;
 }
 
-// w[j][i] = x_i . y_j for i, j < TP (rows of pitch QP), 4 x 4 per thread;
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+
+// w[j][i] = x_i . y_j for j <= i < TP (rows of pitch QP), R x R per thread;
 // `f(i, j, dot)` gives the value that is stored.
-template <int DK, int NT, int QP, typename F>
-__device__ __forceinline__ void pair_products(const float* x, const float* y, float* w, int TP, int WP, F f) {
+template <int R, int DK, int NT, int QP, typename F>
+__device__ __forceinline__ void pair_tiles(const float* x, const float* y, float* w, int TP, int WP, F f) {
   constexpr int NJ = 16, NI = NT / NJ;
   const int tj = threadIdx.x % NJ, ti = threadIdx.x / NJ;
-  for (int ib = 0; ib < TP; ib += 4 * NI)
-    for (int jb = 0; jb < TP && jb < ib + 4 * NI; jb += 4 * NJ) {
-      float acc[4][4] = {};
-      const float* xr[4];
-      const float* yr[4];
+  for (int ib = 0; ib < TP; ib += R * NI)
+    for (int jb = 0; jb < TP && jb < ib + R * NI; jb += R * NJ) {
+      float acc[R][R] = {};
+      const float* xr[R];
+      const float* yr[R];
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
+      for (int a = 0; a < R; ++a) {
         xr[a] = x + min(ib + ti + NI * a, TP - 1) * QP;
         yr[a] = y + min(jb + tj + NJ * a, TP - 1) * QP;
       }
+#pragma unroll 4
       for (int r = 0; r < DK; r += 4) {
-        float4 xv[4], yv[4];
+        float4 xv[R], yv[R];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
+        for (int a = 0; a < R; ++a) {
           xv[a] = *reinterpret_cast<const float4*>(xr[a] + r);
           yv[a] = *reinterpret_cast<const float4*>(yr[a] + r);
         }
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < R; ++a)
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
+          for (int b = 0; b < R; ++b) {
             acc[a][b] = fmaf(xv[a].x, yv[b].x, acc[a][b]);
             acc[a][b] = fmaf(xv[a].y, yv[b].y, acc[a][b]);
             acc[a][b] = fmaf(xv[a].z, yv[b].z, acc[a][b]);
@@ -108,23 +123,35 @@ __device__ __forceinline__ void pair_products(const float* x, const float* y, fl
           }
       }
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
+      for (int a = 0; a < R; ++a)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < R; ++b) {
           const int i = ib + ti + NI * a, j = jb + tj + NJ * b;
           if (i < TP && j < TP) w[j * WP + i] = f(i, j, acc[a][b]);
         }
     }
 }
 
+// Tiles that fit the tree: with few nodes a large tile is mostly its clamped
+// edge (13 nodes of 64 keys in 4 x 4 tiles: a third of the call).
+template <int DK, int NT, int QP, typename F>
+__device__ __forceinline__ void pair_products(const float* x, const float* y, float* w, int TP, int WP, F f) {
+  if (TP <= 16)
+    pair_tiles<1, DK, NT, QP>(x, y, w, TP, WP, f);
+  else if (TP <= 32)
+    pair_tiles<2, DK, NT, QP>(x, y, w, TP, WP, f);
+  else
+    pair_tiles<4, DK, NT, QP>(x, y, w, TP, WP, f);
+}
+
 template <int DK, int DV, typename T, bool kDelta>
-__global__ void __launch_bounds__(TreeShape<DK, DV>::NT)
+__global__ void __launch_bounds__(TreeShape<DK, DV>::NT, 2)
 tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const T* __restrict__ q,
                  const T* __restrict__ k, const T* __restrict__ v, const int* __restrict__ parent,
                  const int* __restrict__ count, T* __restrict__ out, int H, int ntok,
                  const float* __restrict__ alpha, float eps) {
   using Sh = TreeShape<DK, DV>;
-  constexpr int NT = Sh::NT, CG = Sh::CG, RG = Sh::RG, E = Sh::E, NB = Sh::NB, QP = Sh::QP;
+  constexpr int NT = Sh::NT, CG = Sh::CG, RG = Sh::RG, E = Sh::E, NW = Sh::NW, QP = Sh::QP, NB = TreeSmem<DK, DV, kDelta>::NB;
   extern __shared__ __align__(16) float sm[];
   const long long bh = blockIdx.x;
   const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x;
@@ -153,21 +180,29 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   const T* qb = q + bh * (long long)ntok * DK;
   const T* kb = k + bh * (long long)ntok * DK;
   const T* vb = v + bh * (long long)ntok * DV;
-  for (int x = tid; x < TP * DK; x += NT) {
-    const int i = x / DK, r = x % DK;
-    float a = 0.f, c = 0.f;
-    if (i < n) {
-      a = to_f32<T>(qb[x]);
-      c = to_f32<T>(kb[x]);
-      if (!kDelta) {
-        a = phi(a);
-        c = phi(c);
+  // rows, four values at a time, several loads of a thread in flight
+  auto load_rows = [&](const T* src, int width, int pitch, float* dst, bool map) {
+    constexpr int U = 4;
+    const int per = width / 4, all = TP * per;
+    for (int x0 = tid; x0 < all; x0 += U * NT) {
+      float4 f[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + u * NT;
+        f[u] = x < n * per ? load4<T>(src + 4 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + u * NT;
+        if (x >= all) break;
+        if (map && x < n * per) f[u] = make_float4(phi(f[u].x), phi(f[u].y), phi(f[u].z), phi(f[u].w));
+        *reinterpret_cast<float4*>(dst + (x / per) * pitch + 4 * (x % per)) = f[u];
       }
     }
-    fq[i * QP + r] = a;
-    fk[i * QP + r] = c;
-  }
-  for (int x = tid; x < TP * DV; x += NT) vs[x] = x / DV < n ? to_f32<T>(vb[x]) : 0.f;
+  };
+  load_rows(qb, DK, QP, fq, !kDelta);
+  load_rows(kb, DK, QP, fk, !kDelta);
+  load_rows(vb, DV, DV, vs, false);
   if (tid < 32) tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, up);
   if (!kDelta) {
     for (int r = tid; r < DK; r += NT) sm[L.z + r] = z[bh * DK + r];
@@ -195,22 +230,41 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
       for (int i = 0; i < m; ++i) {
         const float* row = x + (i0 + i) * QP + rg * E;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float xr[E];
+        if constexpr (E % 4 == 0) {
+#pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(row + e);
+            xr[e] = f.x; xr[e + 1] = f.y; xr[e + 2] = f.z; xr[e + 3] = f.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) xr[e] = row[e];
+        }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float c = row[e];
+          const float c = xr[e];
           acc.x = fmaf(c, s[e].x, acc.x);
           acc.y = fmaf(c, s[e].y, acc.y);
           acc.z = fmaf(c, s[e].z, acc.z);
           acc.w = fmaf(c, s[e].w, acc.w);
         }
-        *reinterpret_cast<float4*>(part + (i * RG + rg) * DV + 4 * cg) = acc;
+        // the row groups of a warp first
+#pragma unroll
+        for (int o = CG; o < 32; o <<= 1) {
+          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+        }
+        if ((tid & 31) < CG) *reinterpret_cast<float4*>(part + (i * NW + (tid >> 5)) * DV + 4 * cg) = acc;
       }
       __syncthreads();
       for (int x2 = tid; x2 < m * DV; x2 += NT) {
         const int i = x2 / DV, c = x2 % DV;
         float t = 0.f;
 #pragma unroll
-        for (int r = 0; r < RG; ++r) t += part[(i * RG + r) * DV + c];
+        for (int r = 0; r < NW; ++r) t += part[(i * NW + r) * DV + c];
         put((i0 + i) * DV + c, t);
       }
     }
@@ -220,14 +274,15 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   __syncthreads();
 
   if constexpr (kDelta) {
-    // u_j over column c, one thread each: row j needs the rows above it
+    // u_j over column c, one thread each: row j needs the rows on its path
     const float* at = sm + L.w2;
     for (int c = tid; c < DV; c += NT)
       for (int j = 0; j < n; ++j) {
         float u = vs[j * DV + c];
-        const unsigned long long m = mask[j];
-        for (int l = 0; l < j; ++l)
-          if ((m >> l) & 1) u = fmaf(-at[l * WP + j], vs[l * DV + c], u);
+        for (unsigned long long m = mask[j] & ((1ull << j) - 1); m != 0ull; m &= m - 1) {
+          const int l = __ffsll((long long)m) - 1;
+          u = fmaf(-at[l * WP + j], vs[l * DV + c], u);
+        }
         vs[j * DV + c] = u;
       }
     __syncthreads();
@@ -260,13 +315,13 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
         acc[a].x *= p; acc[a].y *= p; acc[a].z *= p; acc[a].w *= p;
       }
     }
-    const int last = min(i0 + 3, n - 1);
-    for (int j = 0; j <= last; ++j) {
+    // the nodes on any of the four paths; one off a node's own path is left
+    // out, not weighted by 0: its values may be infinite or NaN
+    for (unsigned long long any = m[0] | m[1] | m[2] | m[3]; any != 0ull; any &= any - 1) {
+      const int j = __ffsll((long long)any) - 1;
       const float4 w4 = *reinterpret_cast<const float4*>(wt + j * WP + i0);
       const float4 x = *reinterpret_cast<const float4*>(vs + j * DV + 4 * cg);
       const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-      // a node off the path is left out, not weighted by 0: its values may be
-      // infinite or NaN
 #pragma unroll
       for (int a = 0; a < 4; ++a)
         if ((m[a] >> j) & 1) {
@@ -307,8 +362,9 @@ cudaError_t launch(const TreeArgs& a) {
 template <int DK, int DV>
 cudaError_t pick(const TreeArgs& a) {
   // the largest tree's layout fits one SM's shared memory
-  constexpr int kMost = 232448;
-  if (TreeSmem<DK, DV, true>(kTreeMax).total * (int)sizeof(float) > kMost) return cudaErrorInvalidConfiguration;
+  constexpr int kMost = 232448 / (int)sizeof(float);
+  static_assert(TreeSmem<DK, DV, true>(kTreeMax).total <= kMost && TreeSmem<DK, DV, false>(kTreeMax).total <= kMost,
+                "shared memory budget");
   if (a.z == nullptr)
     return a.dtype == LA_BF16 ? launch<DK, DV, __nv_bfloat16, true>(a) : launch<DK, DV, float, true>(a);
   return a.dtype == LA_BF16 ? launch<DK, DV, __nv_bfloat16, false>(a) : launch<DK, DV, float, false>(a);
