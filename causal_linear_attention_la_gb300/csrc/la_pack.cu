@@ -72,7 +72,6 @@ pack_kernel(const float* __restrict__ S, const float* __restrict__ z, unsigned c
   const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
   const int to = slot[b];
   if (to < 0 || to >= slots) return;
-  if (overwritten(slot, b, B)) return;
   const float* src = S + (long long)b * words;
   unsigned char* dc = codes + (long long)to * words;
   unsigned char* ds = scales + (long long)to * (words / W);
@@ -81,8 +80,9 @@ pack_kernel(const float* __restrict__ S, const float* __restrict__ z, unsigned c
 #pragma unroll
   for (int u = 0; u < PU; ++u) {
     const int at = base + u * PT * 4;
-    x[u] = at < words ? *reinterpret_cast<const float4*>(src + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[u] = at < words ? __ldcs(reinterpret_cast<const float4*>(src + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  if (overwritten(slot, b, B)) return;            // (with the loads on their way)
 #pragma unroll
   for (int u = 0; u < PU; ++u) {
     const int at = base + u * PT * 4;
@@ -131,7 +131,7 @@ unpack_kernel(float* __restrict__ S, float* __restrict__ z, const unsigned char*
     q.__x = c[u];
     float4 x = static_cast<float4>(q);
     const float r = pow2((int)e[u] - 127);
-    if (at < words) *reinterpret_cast<float4*>(dst + at) = make_float4(x.x * r, x.y * r, x.z * r, x.w * r);
+    if (at < words) __stcs(reinterpret_cast<float4*>(dst + at), make_float4(x.x * r, x.y * r, x.z * r, x.w * r));
   }
   if (tile == 0 && z != nullptr)
     for (int i = threadIdx.x; i < zwords; i += PT) z[(long long)b * zwords + i] = z_pool[(long long)from * zwords + i];
