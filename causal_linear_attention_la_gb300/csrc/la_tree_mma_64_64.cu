@@ -4,8 +4,9 @@
 
 namespace la {
 cudaError_t tree_mma_64_64(const TreeArgs& a) {
-  if (a.T <= treesmall::TP)
-    return a.z == nullptr ? treesmall::launch<64, 64, true>(a) : treesmall::launch<64, 64, false>(a);
-  return a.z == nullptr ? treewide::launch<64, 64, true>(a) : treewide::launch<64, 64, false>(a);
+  const bool delta = a.z == nullptr;
+  if (a.T <= treesmall::TP) return delta ? treesmall::launch<64, 64, true>(a) : treesmall::launch<64, 64, false>(a);
+  if (a.T <= 32) return delta ? treewide::launch<64, 64, 32, true>(a) : treewide::launch<64, 64, 32, false>(a);
+  return delta ? treewide::launch<64, 64, 64, true>(a) : treewide::launch<64, 64, 64, false>(a);
 }
 }  // namespace la

@@ -29,9 +29,15 @@ namespace {
 template <int DK, int DV>
 struct TreeShape {
   static constexpr int CG = DV / 4;                              // float4 column groups
-  static constexpr int NT = (CG * DK) < 256 ? (CG * DK) : 256;   // threads
+  // threads: 128 for the small heads, whose phases are short (2048 states of 32
+  // nodes at d = 32: 57 us with 256, 45 with 128; 64 nodes 117 and 123)
+  static constexpr int NT = (CG * DK) < 128 ? (CG * DK) : DK * DV <= 1024 ? 128 : 256;
   static constexpr int RG = NT / CG;                             // row groups
   static constexpr int E = DK / RG;                              // state rows per thread
+  // CTAs per SM that the registers allow: two where a thread holds 64 of them
+  // for the state, else four of 256 threads (1536 states of 24 nodes at d = 64,
+  // delta rule: 113 us with two, 92 with four)
+  static constexpr int CTAS = E >= 16 ? 2 : 1024 / NT;
   static constexpr int NW = NT / 32;                             // warps: row groups after a warp's own have met
   static constexpr int QP = DK + 4;                              // pitch of q and k rows (bank-conflict free)
 };
@@ -145,7 +151,7 @@ __device__ __forceinline__ void pair_products(const float* x, const float* y, fl
 }
 
 template <int DK, int DV, typename T, bool kDelta>
-__global__ void __launch_bounds__(TreeShape<DK, DV>::NT, 2)
+__global__ void __launch_bounds__(TreeShape<DK, DV>::NT, TreeShape<DK, DV>::CTAS)
 tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const T* __restrict__ q,
                  const T* __restrict__ k, const T* __restrict__ v, const int* __restrict__ parent,
                  const int* __restrict__ count, T* __restrict__ out, int H, int ntok,

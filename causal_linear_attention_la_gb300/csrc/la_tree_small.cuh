@@ -271,7 +271,10 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
 
   // ---- read: D[c][i] = sum_r S[r][c] x_i[r]
   const bool here = sm100::mbar_drain(bar, 0, kWaitNs);
-  if (!here && lane == 0) atomicExch(status, (int)LA_ERR_TIMEOUT);
+  if (!here) {
+    if (lane == 0) atomicExch(status, (int)LA_ERR_TIMEOUT);
+    (void)sm100::mbar_drain(bar, 0, kWaitNs);      // nothing in flight when the CTA ends
+  }
   const int c0 = 16 * warp + 2 * g;
   float acc[2][4] = {}, acck[2][4] = {};           // (acck: delta rule)
   uint32_t vr[2][2];                               // delta: this lane's values of v

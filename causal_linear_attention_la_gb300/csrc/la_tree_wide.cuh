@@ -16,9 +16,9 @@
 //           in different banks) through two buffers; a slab is used for all
 //           nodes at once
 //   path    D += V^T W^T in steps of 16 nodes, out
-// Up to 48 nodes the slabs have buffers of their own and start with the CTA;
-// above, two CTAs per SM leave no room and the buffers are where phi(k) was,
-// from the pairs on. (The state straight from global memory into the lanes'
+// Up to 32 nodes three CTAs share an SM, slabs of 16 rows. Up to 48 nodes the
+// slabs have buffers of their own and start with the CTA; above, two CTAs per
+// SM leave no room and the buffers are where phi(k) was, from the pairs on. (The state straight from global memory into the lanes'
 // registers, as fragments of 64 bytes, cost twice the wavefronts and 64
 // registers a thread: 79 us on 1536 decay-gated states of up to 64 nodes.)
 //
@@ -34,11 +34,10 @@ namespace treewide {
 
 using namespace treeops;
 
-constexpr int SLAB = 32;                       // state rows per slab
-constexpr int TM = 64;                         // most nodes
-
-template <int DK, int DV, bool kDelta>
+// TM: most nodes, 32 or 64
+template <int DK, int DV, int TM, bool kDelta>
 struct Wide {
+  static constexpr int SLAB = TM == 32 ? 16 : 32;        // state rows per slab
   static constexpr int NT = 2 * DV, NW = DV / 16;
   static constexpr int SLABS = DK / SLAB;
   static constexpr int BUF = SLAB * DV * 4;              // bytes of a slab
@@ -50,7 +49,7 @@ struct Wide {
       : ring(0), qh(0), ql(0), kh(0), kl(0), v(0), wh(0), wl(0), ah(0), al(0), tri(0), mask(0), depth(0), up(0), pw(0),
         zq(0), den(0), rden(0), bad(0), bar(0), total(0), overlay(false) {
     int at = 0;
-    overlay = !kDelta && TP > 48 && 2 * TP * QP >= 2 * BUF;
+    overlay = !kDelta && TM == 64 && TP > 48 && 2 * TP * QP >= 2 * BUF;
     if (!overlay) at += 2 * BUF;
     kh = at;
     at += TP * QP;
@@ -101,15 +100,15 @@ struct Wide {
   }
 };
 
-template <int DK, int DV, bool kDelta>
-__global__ void __launch_bounds__(2 * DV + 32, DV == 128 ? 2 : 3)
+template <int DK, int DV, int TM, bool kDelta>
+__global__ void __launch_bounds__(2 * DV + 32, (DV == 128 ? 2 : 3) + (TM == 32 ? 1 : 0))
 tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restrict__ S, const float* __restrict__ z,
                  const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
                  const __nv_bfloat16* __restrict__ v, const int* __restrict__ parent, const int* __restrict__ count,
                  __nv_bfloat16* __restrict__ out, int H, int ntok, const float* __restrict__ alpha, float eps,
                  int* status) {
-  using Sh = Wide<DK, DV, kDelta>;
-  constexpr int NT = Sh::NT, NW = Sh::NW, SLABS = Sh::SLABS, BUF = Sh::BUF, QP = Sh::QP, VP = Sh::VP, WP = Sh::WP,
+  using Sh = Wide<DK, DV, TM, kDelta>;
+  constexpr int NT = Sh::NT, NW = Sh::NW, SLAB = Sh::SLAB, SLABS = Sh::SLABS, BUF = Sh::BUF, QP = Sh::QP, VP = Sh::VP, WP = Sh::WP,
                 KS = DK / 16, NTM = TM / 8;
   extern __shared__ __align__(1024) uint8_t sm[];
   const long long bh = blockIdx.x;
@@ -169,8 +168,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
   } else {
     // ---- rows: batches of up to four passes, all loads of a batch in flight
     constexpr int CH = DK / 8, RPP = NT / CH, CHV = DV / 8, RPV = NT / CHV;
-    constexpr int PB = TM / RPP < 4 ? TM / RPP : 4, PV = 4;
-    static_assert(RPV * PV == TM, "one batch of v");
+    constexpr int PB = TM / RPP < 4 ? (TM + RPP - 1) / RPP : 4, PV = TM / RPV;
     const int ch = tid % CH, chv = tid % CHV;
     uint4 xv[PV];
     if (!kDelta) {
@@ -534,26 +532,27 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
   }
 }
 
-template <int DK, int DV, bool kDelta>
+template <int DK, int DV, int TM, bool kDelta>
 cudaError_t launch(const TreeArgs& a) {
-  using Sh = Wide<DK, DV, kDelta>;
-  constexpr Sh most(TM), middle(48);
-  // two CTAs per SM (228 KiB, 1 KiB of it taken by each CTA)
-  static_assert(most.total + 1024 <= 116736 && middle.total + 1024 <= 116736, "shared memory of two CTAs");
+  using Sh = Wide<DK, DV, TM, kDelta>;
+  constexpr Sh most(TM), middle(TM == 32 ? 32 : 48);
+  constexpr int bytes = most.total > middle.total ? most.total : middle.total;
+  // two CTAs per SM, three for 32 nodes (228 KiB, 1 KiB of it taken by each CTA)
+  static_assert(bytes + 1024 <= (TM == 32 ? 77824 : 116736), "shared memory of an SM's CTAs");
   static_assert(!kDelta || (TM * (2 * (TM + 1) + DV) * 4 <= most.mask && 32 * (2 * 33 + DV) * 4 <= Sh(32).mask &&
-                            48 * (2 * 49 + DV) * 4 <= middle.mask),
+                            (TM == 32 || 48 * (2 * 49 + DV) * 4 <= middle.mask)),
                 "room for delta_tree_by_paths");
-  static_assert(most.ring % 1024 == 0, "the swizzle goes by address bits");
+  static_assert(most.ring % 1024 == 0 && Sh::BUF % 1024 == 0, "the swizzle goes by address bits");
   const Sh L((a.T + 15) & ~15);
-  auto kern = tree_wide_kernel<DK, DV, kDelta>;
+  auto kern = tree_wide_kernel<DK, DV, TM, kDelta>;
   static KernelOnce once;
   int resident = 0;
-  cudaError_t e = once.prepare(kern, Sh::NT + 32, most.total > middle.total ? most.total : middle.total, &resident);
+  cudaError_t e = once.prepare(kern, Sh::NT + 32, bytes, &resident);
   if (e != cudaSuccess) return e;
   int* status = device_status_ptr();
   if (status == nullptr) return cudaErrorNotReady;
   CUtensorMap map_s;
-  e = state_map<DK, DV>(&map_s, a.S, a.BH, SLAB);
+  e = state_map<DK, DV>(&map_s, a.S, a.BH, Sh::SLAB);
   if (e != cudaSuccess) return e;
   kern<<<a.BH, Sh::NT + 32, L.total, a.stream>>>(map_s, a.S, a.z, (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.k,
                                                  (const __nv_bfloat16*)a.v, a.parent, a.count, (__nv_bfloat16*)a.out,
