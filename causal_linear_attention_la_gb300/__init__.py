@@ -691,8 +691,8 @@ def _rows3(t, name):
 
 
 def _on(device, call, *args):
-    """call(*args, stream) with CUDA device number ``device`` current, on its
-    current stream."""
+    """C entry point ``call``(*args, stream) with CUDA device number ``device``
+    current, on its current stream."""
     import torch
     stream = torch._C._cuda_getCurrentRawStream(device)
     if torch.cuda.current_device() == device:
@@ -723,7 +723,7 @@ def decode_tree(S, z, q, k, v, parent, alpha=None, eps=1e-6, count=None, out=Non
     _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("z", z, f32, (B, H, dk)), ("q", q, q.dtype, (B, H, T, dk)),
                ("k", k, q.dtype, (B, H, T, dk)), ("v", v, q.dtype, (B, H, T, dv)), ("parent", parent, i32, (B, T)),
                ("alpha", alpha, f32, (H,)), ("count", count, i32, (B,)), ("out", out, q.dtype, (B, H, T, dv)))
-    _on(dev, la_decode_tree, S.data_ptr(), z.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _on(dev, lib().la_decode_tree, S.data_ptr(), z.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
         parent.data_ptr(), _ptr(count), out.data_ptr(), B, H, T, dk, dv, _ptr(alpha), eps, code)
     return out
 
@@ -741,7 +741,7 @@ def decode_tree_delta(S, q, k, v, parent, count=None, out=None):
     _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("q", q, q.dtype, (B, H, T, dk)), ("k", k, q.dtype, (B, H, T, dk)),
                ("v", v, q.dtype, (B, H, T, dv)), ("parent", parent, i32, (B, T)), ("count", count, i32, (B,)),
                ("out", out, q.dtype, (B, H, T, dv)))
-    _on(dev, la_decode_tree_delta, S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), parent.data_ptr(),
+    _on(dev, lib().la_decode_tree_delta, S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), parent.data_ptr(),
         _ptr(count), out.data_ptr(), B, H, T, dk, dv, code)
     return out
 
@@ -758,7 +758,7 @@ def verify_chain(target, draft, tokens, uniform, count=None):
                ("tokens", tokens, i32, (B, T)), ("uniform", uniform, torch.float32, (B, T + 1)), ("count", count, i32, (B,)))
     accepted = torch.empty((B,), dtype=i32, device=target.device)
     nxt = torch.empty((B,), dtype=i32, device=target.device)
-    _on(dev, la_verify_chain, target.data_ptr(), draft.data_ptr(), tokens.data_ptr(), _ptr(count),
+    _on(dev, lib().la_verify_chain, target.data_ptr(), draft.data_ptr(), tokens.data_ptr(), _ptr(count),
         uniform.data_ptr(), accepted.data_ptr(), nxt.data_ptr(), B, T, V, code)
     return accepted, nxt
 
@@ -777,7 +777,7 @@ def verify_tree(target, tokens, parent, uniform, count=None):
     path = torch.empty((B, T), dtype=i32, device=target.device)
     accepted = torch.empty((B,), dtype=i32, device=target.device)
     nxt = torch.empty((B,), dtype=i32, device=target.device)
-    _on(dev, la_verify_tree, target.data_ptr(), tokens.data_ptr(), parent.data_ptr(), _ptr(count),
+    _on(dev, lib().la_verify_tree, target.data_ptr(), tokens.data_ptr(), parent.data_ptr(), _ptr(count),
         uniform.data_ptr(), path.data_ptr(), accepted.data_ptr(), nxt.data_ptr(), B, T, V, code)
     return path, accepted, nxt
 
@@ -800,7 +800,7 @@ def state_advance(S, z, k, v, path=None, accepted=None, alpha=None, S_out=None, 
     _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("z", z, f32, (B, H, dk)), ("k", k, k.dtype, (B, H, T, dk)),
                ("v", v, k.dtype, (B, H, T, dv)), ("path", path, i32, (B, T)), ("accepted", accepted, i32, (B,)),
                ("alpha", alpha, f32, (H,)), ("S_out", S_out, f32, (B, H, dk, dv)), ("z_out", z_out, f32, (B, H, dk)))
-    _on(dev, la_state_advance, S.data_ptr(), z.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(path), _ptr(accepted),
+    _on(dev, lib().la_state_advance, S.data_ptr(), z.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(path), _ptr(accepted),
         S_out.data_ptr(), z_out.data_ptr(), B, H, T, dk, dv, _ptr(alpha), code)
     return S_out, z_out
 
@@ -816,7 +816,7 @@ def state_advance_delta(S, k, v, path=None, accepted=None, S_out=None):
         S_out = S
     _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("k", k, k.dtype, (B, H, T, dk)), ("v", v, k.dtype, (B, H, T, dv)),
                ("path", path, i32, (B, T)), ("accepted", accepted, i32, (B,)), ("S_out", S_out, f32, (B, H, dk, dv)))
-    _on(dev, la_state_advance_delta, S.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(path), _ptr(accepted),
+    _on(dev, lib().la_state_advance_delta, S.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(path), _ptr(accepted),
         S_out.data_ptr(), B, H, T, dk, dv, code)
     return S_out
 
@@ -848,7 +848,7 @@ def state_pack(S, codes, scales, slot, z=None, z_pool=None):
     int32 of a pool (state_pool): 8-bit codes with a power-of-two scale per
     block of min(32, dv) values (la_state_pack)."""
     B, H, dk, dv, slots = _pool_args(S, z, codes, scales, z_pool, slot)
-    _on(S.get_device(), la_state_pack, S.data_ptr(), _ptr(z), codes.data_ptr(), scales.data_ptr(), _ptr(z_pool),
+    _on(S.get_device(), lib().la_state_pack, S.data_ptr(), _ptr(z), codes.data_ptr(), scales.data_ptr(), _ptr(z_pool),
         slot.data_ptr(), B, H, dk, dv, slots)
 
 
@@ -856,6 +856,6 @@ def state_unpack(codes, scales, slot, S, z_pool=None, z=None):
     """The states of slots ``slot`` [B] int32 back into S [B,H,dk,dv] (and z)
     (la_state_unpack); sequences whose slot is outside the pool keep theirs."""
     B, H, dk, dv, slots = _pool_args(S, z, codes, scales, z_pool, slot)
-    _on(S.get_device(), la_state_unpack, codes.data_ptr(), scales.data_ptr(), _ptr(z_pool), slot.data_ptr(),
+    _on(S.get_device(), lib().la_state_unpack, codes.data_ptr(), scales.data_ptr(), _ptr(z_pool), slot.data_ptr(),
         S.data_ptr(), _ptr(z), B, H, dk, dv, slots)
     return S

@@ -368,7 +368,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
     const uint8_t* box = sm + L.ring + (warp >> 1) * (SLAB * 128) + (g & 1) * 8;
     const uint8_t* even = box + 2 * t * 128 + ((piece ^ (2 * t)) << 4);
     const uint8_t* odd = box + (2 * t + 1) * 128 + ((piece ^ (2 * t + 1)) << 4);
-#pragma unroll 1
+#pragma unroll
     for (int s = 0; s < SLABS; ++s) {
       (void)sm100::mbar_drain(full + (s & 1), (s >> 1) & 1, kWaitNs);
 #pragma unroll
