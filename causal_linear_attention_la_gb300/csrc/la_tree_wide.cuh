@@ -11,19 +11,24 @@
 //   pairs   16 x 16 tiles of node pairs on and below the diagonal, dealt to
 //           the warps; mask and decay applied, W stored as hi and lo, row sums
 //           per tile
-//   read    D = S^T x: the state comes by TMA in slabs of 32 rows (boxes of 32
-//           columns with the 128-byte swizzle, so that a fragment's rows lie
-//           in different banks) through two buffers; a slab is used for all
-//           nodes at once
+//   read    D = S^T x: the state comes by TMA in slabs of 16 or 32 rows (boxes
+//           of 32 columns with the 128-byte swizzle, so that a fragment's rows
+//           lie in different banks) through two buffers; a slab is used for
+//           all nodes at once
 //   path    D += V^T W^T in steps of 16 nodes, out
-// Up to 32 nodes three CTAs share an SM, slabs of 16 rows. Up to 48 nodes the
-// slabs have buffers of their own and start with the CTA; above, two CTAs per
-// SM leave no room and the buffers are where phi(k) was, from the pairs on. (The state straight from global memory into the lanes'
-// registers, as fragments of 64 bytes, cost twice the wavefronts and 64
-// registers a thread: 79 us on 1536 decay-gated states of up to 64 nodes.)
+// Up to 32 nodes three CTAs share an SM and slabs have 16 rows. Up to 48 nodes
+// the slabs have buffers of their own and start with the CTA; above, two CTAs
+// per SM leave no room and the buffers are where phi(k) was, from the pairs on.
+// 1536 decay-gated d = 128 states of up to 64 nodes: 59 us, the tensor pipe at
+// 0.29, the issue slots at 0.41 - chains of dependent steps. What did not help:
+// the state straight from global memory into the lanes' registers (fragments
+// of 64 bytes, twice the wavefronts: 79 us), two warps per 16 columns (half as
+// many instructions again: 70 us), a ring of four slabs, the whole state at
+// once with two CTAs for 32 nodes (51 us for 1536 full trees, three CTAs 47),
+// CTAs of an SM started apart.
 //
 // The delta rule reads for keys and queries in one pass over the slabs and
-// solves for u in registers (la_tree_ops.cuh) while the extra warp has inverted
+// solves for u in registers (la_tree_ops.cuh) after the extra warp has inverted
 // the diagonal blocks.
 #pragma once
 
