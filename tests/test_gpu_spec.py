@@ -120,6 +120,69 @@ def test_tree(B, H, T, dk, dv, rule, dtype):
 
 
 @pytest.mark.parametrize("rule", ["plain", "decay", "delta"])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+def test_tree_sizes_on_tensor_cores(dk, dv, rule):
+    """Both sides of every size at which the tensor-core kernels change (16, 32,
+    48 and 64 nodes, halves and whole blocks of 16), as one path, as a star and
+    as a random tree."""
+    H = 2
+    delta = rule == "delta"
+    alpha = np.array([0.7, 0.95], np.float32) if rule == "decay" else None
+    for T in (1, 8, 9, 15, 16, 17, 24, 25, 31, 32, 33, 41, 48, 49, 56, 57, 63, 64):
+        B = 3
+        S, z = state(B, H, dk, dv, T, delta)
+        q, k, v = rows(B, H, T, dk, dv, T + 1, "bf16", delta)
+        parent = np.stack([np.arange(T) - 1, np.full(T, -1), tree(1, T, T)[0]])
+        args = [to_dev(x, "bf16") for x in (q, k, v)] + [i32(parent)]
+        if delta:
+            out = la.decode_tree_delta(cuda(S), *args)
+            want, scale = spec.decode_tree_delta(S, q, k, v, parent)
+        else:
+            out = la.decode_tree(cuda(S), cuda(z), *args, alpha=None if alpha is None else cuda(alpha))
+            want, scale = spec.decode_tree(S, z, q, k, v, parent, alpha)
+        near(to_host(out), want, scale, "bf16", gamma(dk, T if delta else 1, True))
+
+
+@pytest.mark.parametrize("rule", ["plain", "decay", "delta"])
+def test_tree_of_64_ragged(rule):
+    """Trees of every size class in one call of 64 rows; rows behind them stay."""
+    B, H, T, d = 10, 2, 64, 128
+    delta = rule == "delta"
+    count = [0, 1, 8, 16, 17, 32, 33, 48, 49, 64]
+    alpha = np.array([0.5, 1.0], np.float32) if rule == "decay" else None
+    S, z = state(B, H, d, d, 44, delta)
+    q, k, v = rows(B, H, T, d, d, 45, "bf16", delta)
+    for b, n in enumerate(count):
+        q[b, :, n:], k[b, :, n:], v[b, :, n:] = np.nan, np.inf, np.nan
+    parent = tree(B, T, 46, lean=0.2)
+    args = [to_dev(x, "bf16") for x in (q, k, v)] + [i32(parent)]
+    out = to_dev(np.full((B, H, T, d), -3.0, np.float32), "bf16")
+    if delta:
+        la.decode_tree_delta(cuda(S), *args, count=i32(count), out=out)
+        want, scale = spec.decode_tree_delta(S, q, k, v, parent, count)
+    else:
+        la.decode_tree(cuda(S), cuda(z), *args, alpha=None if alpha is None else cuda(alpha), count=i32(count), out=out)
+        want, scale = spec.decode_tree(S, z, q, k, v, parent, alpha, count)
+    got = to_host(out)
+    for b, n in enumerate(count):
+        assert np.all(got[b, :, n:] == -3.0)
+        near(got[b, :, :n], want[b, :, :n], scale[b, :, :n], "bf16", gamma(d, T if delta else 1, True))
+
+
+def test_tree_repeats_bit_for_bit():
+    import torch
+    B, H, T, d = 40, 8, 40, 128
+    S, z = (cuda(x) for x in state(B, H, d, d, 50))
+    q, k, v = (to_dev(x, "bf16") for x in rows(B, H, T, d, d, 51, "bf16"))
+    parent = i32(tree(B, T, 52))
+    one = la.decode_tree(S, z, q, k, v, parent)
+    two = la.decode_tree_delta(S, q, k, v, parent)
+    for _ in range(5):
+        assert torch.equal(one, la.decode_tree(S, z, q, k, v, parent))
+        assert torch.equal(two, la.decode_tree_delta(S, q, k, v, parent))
+
+
+@pytest.mark.parametrize("rule", ["plain", "decay", "delta"])
 @pytest.mark.parametrize("T", [1, 5, 16, 24, 47, 64])
 def test_tree_on_cuda_cores_agrees(T, rule):
     """The CUDA-core kernel on bf16 rows of the tensor-core shapes."""
@@ -179,10 +242,11 @@ def test_tree_ragged(delta, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("delta", [False, True])
-def test_tree_nonfinite_rows_off_the_path(delta, d, dtype):
+@pytest.mark.parametrize("T", [14, 24, 60])
+def test_tree_nonfinite_rows_off_the_path(T, delta, d, dtype):
     """Infinities, NaN and the type's largest numbers in one node reach that
     node's descendants and nobody else."""
-    B, H, T = 1, 2, 24
+    B, H = 1, 2
     S, z = state(B, H, d, d, 8, delta)
     q, k, v = rows(B, H, T, d, d, 9, dtype, delta)
     parent = tree(B, T, 10)
@@ -195,7 +259,7 @@ def test_tree_nonfinite_rows_off_the_path(delta, d, dtype):
     else:
         want, scale = spec.decode_tree(S, z, q, k, v, parent)
     for kv in ("v", "k", "kv"):
-        for x in (np.nan, np.inf, -np.inf, 3e38):
+        for x in (np.nan, np.inf, -np.inf, 3e38, -3e38):
             k2, v2 = k.copy(), v.copy()
             if "v" in kv:
                 v2[:, :, bad, ::3] = x
