@@ -266,50 +266,49 @@ __device__ void row_sums(const T* p, const T* q, int V, bool vec, int rank, int 
   cluster_sync();
 }
 
-// By one warp, from row_sums: a lane takes nc / 2 sums in a row (one of 16 for
-// a single CTA).
-__device__ __forceinline__ Found find_part_warp(const VerifyShared& sh, int nc, float u) {
-  const int lane = threadIdx.x & 31, per = nc > 1 ? nc * VW / 32 : 1;
-  const Pair* mine = sh.sums + lane * per;
-  const bool has = lane * per < nc * VW;
-  Pair sum = {0.f, 0.f};
-  for (int i = 0; i < per; ++i)
-    if (has) sum = sum + mine[i];
-  const Pair upto = prefix<32>(sum);
+// By one warp, from row_sums: a lane takes PER sums in a row (nc / 2; one of 16
+// for a single CTA).
+template <int PER>
+__device__ __forceinline__ Found find_part_warp(const VerifyShared& sh, int count, float u) {
+  const int lane = threadIdx.x & 31;
+  Pair c[PER], upto[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] = lane * PER + i < count ? sh.sums[lane * PER + i] : Pair{0.f, 0.f};
+    upto[i] = i == 0 ? c[0] : upto[i - 1] + c[i];
+  }
+  const Pair through = prefix<32>(upto[PER - 1]);
   Found f;
-  f.total = from_lane(upto, 31);
+  f.total = from_lane(through, 31);
   f.want = u * f.total;
-  const bool some = sum.h > 0.f;
-  const unsigned past = __ballot_sync(0xffffffffu, some && upto > f.want);
-  const unsigned any = __ballot_sync(0xffffffffu, some);
+  Pair front = {__shfl_up_sync(0xffffffffu, through.h, 1), __shfl_up_sync(0xffffffffu, through.l, 1)};
+  if (lane == 0) front = {0.f, 0.f};
+  // this lane's first sum that passes, and its last positive one
+  int hit = -1, last = -1;
+  Pair before = front;
+#pragma unroll
+  for (int i = PER - 1; i >= 0; --i)
+    if (c[i].h > 0.f) {
+      if (last < 0) last = i;
+      if (front + upto[i] > f.want) {
+        hit = i;
+        before = i == 0 ? front : front + upto[i > 0 ? i - 1 : 0];
+      }
+    }
+  const unsigned past = __ballot_sync(0xffffffffu, hit >= 0);
+  const unsigned any = __ballot_sync(0xffffffffu, last >= 0);
   f.end = past == 0u;
   const int at = f.end ? (any != 0u ? 31 - __clz(any) : 0) : __ffs(past) - 1;
-  const Pair front = from_lane(upto, at > 0 ? at - 1 : 0);
-  f.before = at > 0 ? front : Pair{0.f, 0.f};
-  // among that lane's sums
-  const Pair* theirs = sh.sums + at * per;
-  int last = 0, hit = -1;
-  sum = f.before;
-  for (int i = 0; i < per && hit < 0; ++i) {
-    const Pair x = theirs[i];
-    if (!(x.h > 0.f)) continue;
-    last = i;
-    const Pair next = sum + x;
-    if (!f.end && next > f.want) {
-      hit = i;
-      f.before = sum;
-    }
-    sum = next;
-  }
-  if (hit < 0) f.end = true;
-  f.part = at * per + (hit < 0 ? last : hit);
+  f.part = at * PER + max(__shfl_sync(0xffffffffu, f.end ? last : hit, at), 0);
+  f.before = from_lane(before, at);
   return f;
 }
 
 // By the CTA: one warp searches (the pair arithmetic of sixteen would queue up).
 __device__ __forceinline__ Found find_part(VerifyShared& sh, int nc, float u) {
   if (threadIdx.x < 32) {
-    const Found f = find_part_warp(sh, nc, u);
+    const Found f = nc == 8 ? find_part_warp<4>(sh, nc * VW, u)
+                    : nc == 4 ? find_part_warp<2>(sh, nc * VW, u) : find_part_warp<1>(sh, nc * VW, u);
     if (threadIdx.x == 0) sh.found_part = f;
   }
   __syncthreads();
