@@ -206,10 +206,11 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
       }
     }
   };
+  // (the masks while the state and the rows are on their way)
+  if (tid >= NT - 32) tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, up);
   load_rows(qb, DK, QP, fq, !kDelta);
   load_rows(kb, DK, QP, fk, !kDelta);
   load_rows(vb, DV, DV, vs, false);
-  if (tid < 32) tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, up);
   if (!kDelta) {
     for (int r = tid; r < DK; r += NT) sm[L.z + r] = z[bh * DK + r];
     const float a = alpha != nullptr ? alpha[h] : 1.f;
@@ -233,6 +234,7 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
     for (int i0 = 0; i0 < n; i0 += NB) {
       const int m = min(NB, n - i0);
       __syncthreads();       // the previous group's partial sums have been read
+#pragma unroll 2
       for (int i = 0; i < m; ++i) {
         const float* row = x + (i0 + i) * QP + rg * E;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -301,7 +303,7 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
       for (int j = tid & 31; j <= i; j += 32) t += wt[j * WP + i];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if ((tid & 31) == 0) sm[L.den + i] = t + eps;
+      if ((tid & 31) == 0) sm[L.den + i] = 1.f / (t + eps);
     }
     __syncthreads();
   }
@@ -325,12 +327,13 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
     // out, not weighted by 0: its values may be infinite or NaN
     for (unsigned long long any = m[0] | m[1] | m[2] | m[3]; any != 0ull; any &= any - 1) {
       const int j = __ffsll((long long)any) - 1;
+      const unsigned long long bit = any & (0ull - any);
       const float4 w4 = *reinterpret_cast<const float4*>(wt + j * WP + i0);
       const float4 x = *reinterpret_cast<const float4*>(vs + j * DV + 4 * cg);
       const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
       for (int a = 0; a < 4; ++a)
-        if ((m[a] >> j) & 1) {
+        if ((m[a] & bit) != 0ull) {
           acc[a].x = fmaf(w[a], x.x, acc[a].x);
           acc[a].y = fmaf(w[a], x.y, acc[a].y);
           acc[a].z = fmaf(w[a], x.z, acc[a].z);
@@ -342,7 +345,7 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
       if (i0 + a >= n) break;
       if (!kDelta) {
         const float d = sm[L.den + i0 + a];
-        acc[a].x /= d; acc[a].y /= d; acc[a].z /= d; acc[a].w /= d;
+        acc[a].x *= d; acc[a].y *= d; acc[a].z *= d; acc[a].w *= d;
       }
       store4<T>(ob + (long long)(i0 + a) * DV + 4 * cg, acc[a]);
     }
