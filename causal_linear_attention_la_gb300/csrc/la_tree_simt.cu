@@ -30,7 +30,8 @@ template <int DK, int DV>
 struct TreeShape {
   static constexpr int CG = DV / 4;                              // float4 column groups
   // threads: 128 for the small heads, whose phases are short (2048 states of 32
-  // nodes at d = 32: 57 us with 256, 45 with 128; 64 nodes 117 and 123)
+  // nodes at d = 32: 57 us with 256, 45 with 128; 64 nodes 117 and 123), 256
+  // from there on (2048 fp32 states of 16 nodes at d = 64: 53 us with 128, 49)
   static constexpr int NT = (CG * DK) < 128 ? (CG * DK) : DK * DV <= 1024 ? 128 : 256;
   static constexpr int RG = NT / CG;                             // row groups
   static constexpr int E = DK / RG;                              // state rows per thread
@@ -42,24 +43,29 @@ struct TreeShape {
   static constexpr int QP = DK + 4;                              // pitch of q and k rows (bank-conflict free)
 };
 
-// Shared-memory layout in floats for T nodes.
+// Shared-memory layout in floats for T nodes of a call with rows for `most`. The
+// read's result takes the place of the k rows, which are done with by then,
+// where its rows fit, and the read's groups are of 8 nodes above 16: more CTAs
+// per SM (1536 fp32 states at d = 64: 24 nodes 59 -> 51 us, 64 nodes 226 -> 152,
+// with the delta rule 526 -> 348; at d = 128 one CTA per SM either way).
 template <int DK, int DV, bool kDelta>
 struct TreeSmem {
-  int TP, WP, q, k, v, w, w2, qs, part, z, den, pw, depth, mask, up, total;
-  static constexpr int NB = kDelta ? 8 : 16;         // nodes per group (the delta rule's layout is the larger)
-  __host__ __device__ constexpr explicit TreeSmem(int T)
-      : TP(0), WP(0), q(0), k(0), v(0), w(0), w2(0), qs(0), part(0), z(0), den(0), pw(0), depth(0), mask(0), up(0), total(0) {
+  int TP, WP, nb, q, k, v, w, w2, qs, part, z, den, pw, depth, mask, up, total;
+  __host__ __device__ constexpr TreeSmem(int T, int most)
+      : TP(0), WP(0), nb(0), q(0), k(0), v(0), w(0), w2(0), qs(0), part(0), z(0), den(0), pw(0), depth(0), mask(0), up(0),
+        total(0) {
     using Sh = TreeShape<DK, DV>;
     TP = (T + 3) & ~3;
+    nb = most <= 16 && !kDelta ? 16 : 8;               // nodes per group of the read
     WP = TP + 4;
     q = 0;
     k = q + TP * Sh::QP;
     v = k + TP * Sh::QP;
     w = v + TP * DV;
     w2 = w + TP * WP;
-    qs = w2 + (kDelta ? TP * WP : 0);
-    part = qs + TP * DV;
-    z = part + NB * Sh::NW * DV;
+    part = w2 + (kDelta ? TP * WP : 0);
+    qs = DV <= Sh::QP ? k : part + nb * Sh::NW * DV;
+    z = part + nb * Sh::NW * DV + (DV <= Sh::QP ? 0 : TP * DV);
     den = z + DK;
     pw = den + TP;
     depth = pw + kTreeMax + 4;
@@ -157,14 +163,14 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
                  const int* __restrict__ count, T* __restrict__ out, int H, int ntok,
                  const float* __restrict__ alpha, float eps) {
   using Sh = TreeShape<DK, DV>;
-  constexpr int NT = Sh::NT, CG = Sh::CG, RG = Sh::RG, E = Sh::E, NW = Sh::NW, QP = Sh::QP, NB = TreeSmem<DK, DV, kDelta>::NB;
+  constexpr int NT = Sh::NT, CG = Sh::CG, RG = Sh::RG, E = Sh::E, NW = Sh::NW, QP = Sh::QP;
   extern __shared__ __align__(16) float sm[];
   const long long bh = blockIdx.x;
   const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x;
   const int n = clamp_count(count, b, ntok);
   if (n == 0) return;
-  const TreeSmem<DK, DV, kDelta> L(n);
-  const int TP = L.TP, WP = L.WP;
+  const TreeSmem<DK, DV, kDelta> L(n, ntok);
+  const int TP = L.TP, WP = L.WP, NB = L.nb;
   float* fq = sm + L.q;
   float* fk = sm + L.k;
   float* vs = sm + L.v;
@@ -352,14 +358,22 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   }
 }
 
+// The largest layout of any call (a call of 16 rows has the longer groups).
+template <int DK, int DV, bool kDelta>
+constexpr int tree_smem_most() {
+  const int a = TreeSmem<DK, DV, kDelta>(16, 16).total, b = TreeSmem<DK, DV, kDelta>(kTreeMax, kTreeMax).total;
+  return a > b ? a : b;
+}
+
 template <int DK, int DV, typename T, bool kDelta>
 cudaError_t launch(const TreeArgs& a) {
-  const int smem = TreeSmem<DK, DV, kDelta>(a.T).total * (int)sizeof(float);
+  const int smem = TreeSmem<DK, DV, kDelta>(a.T, a.T).total * (int)sizeof(float);
   auto kern = tree_simt_kernel<DK, DV, T, kDelta>;
   static KernelOnce once;
   int resident = 0;
-  cudaError_t e = once.prepare(kern, TreeShape<DK, DV>::NT, TreeSmem<DK, DV, kDelta>(kTreeMax).total * (int)sizeof(float),
-                               &resident);
+  constexpr int most = tree_smem_most<DK, DV, kDelta>() * (int)sizeof(float);
+  static_assert(most <= 232448, "shared memory budget");
+  cudaError_t e = once.prepare(kern, TreeShape<DK, DV>::NT, most, &resident);
   if (e != cudaSuccess) return e;
   kern<<<a.BH, TreeShape<DK, DV>::NT, smem, a.stream>>>(a.S, a.z, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.parent,
                                                         a.count, (T*)a.out, a.H, a.T, a.alpha, a.eps);
@@ -370,10 +384,6 @@ cudaError_t launch(const TreeArgs& a) {
 
 template <int DK, int DV>
 cudaError_t pick(const TreeArgs& a) {
-  // the largest tree's layout fits one SM's shared memory
-  constexpr int kMost = 232448 / (int)sizeof(float);
-  static_assert(TreeSmem<DK, DV, true>(kTreeMax).total <= kMost && TreeSmem<DK, DV, false>(kTreeMax).total <= kMost,
-                "shared memory budget");
   if (a.z == nullptr)
     return a.dtype == LA_BF16 ? launch<DK, DV, __nv_bfloat16, true>(a) : launch<DK, DV, float, true>(a);
   return a.dtype == LA_BF16 ? launch<DK, DV, __nv_bfloat16, false>(a) : launch<DK, DV, float, false>(a);
