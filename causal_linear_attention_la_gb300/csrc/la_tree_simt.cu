@@ -14,12 +14,17 @@
 //   out_i = S^T q_i + sum_{j in anc(i)} (q_i.k_j) u_j,
 // whose matrix is lower triangular because a parent comes before its children.
 //
-// One CTA per (batch, head). The state is read once, straight into registers
-// (thread (rg, cg): E rows, four columns, all loads in flight together); the
-// nodes pass by it in groups of NB, the row groups' partial sums meet by
-// shuffles within a warp and then in shared memory. The pair products and the
-// sums over the path are register tiles from shared memory. Everything is
-// fp32; small trees are bound by the chain of these steps.
+// One CTA per (batch, head). The state is read once, straight into registers: a
+// warp holds whole columns (each lane E rows of four), so that the nodes pass by
+// it without a barrier, G at a time, and their sums over the rows meet in the
+// warp, halving what a lane holds at each exchange. The pair products and the
+// sums over the path are register tiles from shared memory. Everything is fp32;
+// small trees are bound by the chain of these steps, large ones by the read's
+// shared-memory loads and exchanges (d = 128: 20 cycles a warp and node against
+// 16 for its arithmetic) with the few warps that the registers leave.
+// 1536 fp32 states: 64 nodes at d = 128 269 us, with the delta rule 387 (350 and
+// 668 with the read's sums met in shared memory and one thread per column in the
+// delta rule's solve); at d = 64 95 and 179 (152 and 348).
 #include "la_tree.cuh"
 
 namespace la {
@@ -29,44 +34,45 @@ namespace {
 template <int DK, int DV>
 struct TreeShape {
   static constexpr int CG = DV / 4;                              // float4 column groups
-  // threads: 128 for the small heads, whose phases are short (2048 states of 32
-  // nodes at d = 32: 57 us with 256, 45 with 128; 64 nodes 117 and 123), 256
-  // from there on (2048 fp32 states of 16 nodes at d = 64: 53 us with 128, 49)
+  // threads: 128 for the small heads, whose phases are short, 256 from there on
+  // (measured before the read took its present form: 2048 states of 32 nodes at
+  // d = 32 57 us with 256, 45 with 128; of 16 at d = 64 in fp32 49 and 53)
   static constexpr int NT = (CG * DK) < 128 ? (CG * DK) : DK * DV <= 1024 ? 128 : 256;
-  static constexpr int RG = NT / CG;                             // row groups
-  static constexpr int E = DK / RG;                              // state rows per thread
-  // CTAs per SM that the registers allow: two where a thread holds 64 of them
-  // for the state, else four of 256 threads (1536 states of 24 nodes at d = 64,
-  // delta rule: 113 us with two, 92 with four)
-  static constexpr int CTAS = E >= 16 ? 2 : 1024 / NT;
-  static constexpr int NW = NT / 32;                             // warps: row groups after a warp's own have met
+  static constexpr int RO = NT / CG;                             // node groups of the output
   static constexpr int QP = DK + 4;                              // pitch of q and k rows (bank-conflict free)
+  // the read: a lane holds E rows of a column group, RL lanes of a warp all of
+  // its rows; RW warps hold the state, the SPLIT copies of it share the nodes
+  static constexpr int E = DK * DV <= 256 ? 2 : DK * DV <= 4096 ? 4 : DK * DV / 1024;
+  static constexpr int RL = DK / E, CW = 32 / RL;
+  static constexpr int RW = CG / CW, SPLIT = NT / 32 / RW;
+  static constexpr int G = RL > 16 ? 8 : 4;                      // nodes at a time
+  // CTAs per SM that the registers are cut for: two where a thread holds 64 of
+  // them for the state; four of 256 threads (1536 fp32 states at d = 64 with four
+  // and three: 16 nodes 32 and 39 us, 24 45 and 52, 64 with the delta rule 179
+  // and 171); six of 128 (d = 32, bf16, with eight and six: 16 nodes 20 and 18,
+  // 64 with the delta rule 102 and 93)
+  static constexpr int CTAS = E >= 16 ? 2 : NT == 128 ? 6 : 1024 / NT;
+  static_assert(RL <= 32 && CW >= 1 && RW * CW == CG && SPLIT >= 1 && SPLIT * RW * 32 == NT, "read layout");
 };
 
-// Shared-memory layout in floats for T nodes of a call with rows for `most`. The
-// read's result takes the place of the k rows, which are done with by then,
-// where its rows fit, and the read's groups are of 8 nodes above 16: more CTAs
-// per SM (1536 fp32 states at d = 64: 24 nodes 59 -> 51 us, 64 nodes 226 -> 152,
-// with the delta rule 526 -> 348; at d = 128 one CTA per SM either way).
+// Shared-memory layout in floats for T nodes. The read's result takes the place
+// of the k rows, which are done with by then, where its rows fit.
 template <int DK, int DV, bool kDelta>
 struct TreeSmem {
-  int TP, WP, nb, q, k, v, w, w2, qs, part, z, den, pw, depth, mask, up, total;
-  __host__ __device__ constexpr TreeSmem(int T, int most)
-      : TP(0), WP(0), nb(0), q(0), k(0), v(0), w(0), w2(0), qs(0), part(0), z(0), den(0), pw(0), depth(0), mask(0), up(0),
-        total(0) {
+  int TP, WP, q, k, v, w, w2, qs, z, den, pw, depth, mask, up, total;
+  __host__ __device__ constexpr explicit TreeSmem(int T)
+      : TP(0), WP(0), q(0), k(0), v(0), w(0), w2(0), qs(0), z(0), den(0), pw(0), depth(0), mask(0), up(0), total(0) {
     using Sh = TreeShape<DK, DV>;
     TP = (T + 3) & ~3;
-    nb = most <= 16 && !kDelta ? 16 : 8;               // nodes per group of the read
     WP = TP + 4;
     q = 0;
     k = q + TP * Sh::QP;
     v = k + TP * Sh::QP;
     w = v + TP * DV;
     w2 = w + TP * WP;
-    part = w2 + (kDelta ? TP * WP : 0);
-    qs = DV <= Sh::QP ? k : part + nb * Sh::NW * DV;
-    z = part + nb * Sh::NW * DV + (DV <= Sh::QP ? 0 : TP * DV);
-    den = z + DK;
+    z = w2 + (kDelta ? TP * WP : 0);
+    qs = DV <= Sh::QP ? k : z + DK;
+    den = z + DK + (DV <= Sh::QP ? 0 : TP * DV);
     pw = den + TP;
     depth = pw + kTreeMax + 4;
     up = depth + TP;
@@ -100,60 +106,88 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
                      __uint_as_float(u.y & 0xffff0000u));
 }
 
-// w[j][i] = x_i . y_j for j <= i < TP (rows of pitch QP), R x R per thread;
-// `f(i, j, dot)` gives the value that is stored.
-template <int R, int DK, int NT, int QP, typename F>
-__device__ __forceinline__ void pair_tiles(const float* x, const float* y, float* w, int TP, int WP, F f) {
+// Two fp32 values in one register pair, and the two-wide FMA: half the
+// instructions of the read (16 nodes at d = 128: 81 us without, 75; in the pair
+// products the registers that it takes cost more than it saves).
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float sum2(uint64_t x) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+  return lo + hi;
+}
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+
+__device__ __forceinline__ void sub_from(float* p, float x) { *p -= x; }
+__device__ __forceinline__ void sub_from(float* p, float4 x) {
+  float4 y = *reinterpret_cast<const float4*>(p);
+  y.x -= x.x; y.y -= x.y; y.z -= x.z; y.w -= x.w;
+  *reinterpret_cast<float4*>(p) = y;
+}
+
+// x_i . y_j of M matrices x against one y, for j <= i < TP (rows of pitch QP),
+// R x R pairs per thread; `f(m, i, j, dot)` stores them. With 256 threads one
+// tile covers the tree and its blocks above the diagonal are left out.
+template <int R, int M, int DK, int NT, int QP, typename F>
+__device__ __forceinline__ void pair_tiles(const float* const (&x)[M], const float* y, int TP, F f) {
   constexpr int NJ = 16, NI = NT / NJ;
   const int tj = threadIdx.x % NJ, ti = threadIdx.x / NJ;
   for (int ib = 0; ib < TP; ib += R * NI)
     for (int jb = 0; jb < TP && jb < ib + R * NI; jb += R * NJ) {
-      float acc[R][R] = {};
-      const float* xr[R];
-      const float* yr[R];
+      float acc[M][R][R] = {};
+      int xr[R], yr[R];
 #pragma unroll
       for (int a = 0; a < R; ++a) {
-        xr[a] = x + min(ib + ti + NI * a, TP - 1) * QP;
-        yr[a] = y + min(jb + tj + NJ * a, TP - 1) * QP;
+        xr[a] = min(ib + ti + NI * a, TP - 1) * QP;
+        yr[a] = min(jb + tj + NJ * a, TP - 1) * QP;
       }
-#pragma unroll 4
+#pragma unroll(M == 1 ? 4 : 2)
       for (int r = 0; r < DK; r += 4) {
-        float4 xv[R], yv[R];
+        float4 yv[R];
 #pragma unroll
-        for (int a = 0; a < R; ++a) {
-          xv[a] = *reinterpret_cast<const float4*>(xr[a] + r);
-          yv[a] = *reinterpret_cast<const float4*>(yr[a] + r);
-        }
+        for (int b = 0; b < R; ++b) yv[b] = *reinterpret_cast<const float4*>(y + yr[b] + r);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int a = 0; a < R; ++a) {
+            const float4 xv = *reinterpret_cast<const float4*>(x[m] + xr[a] + r);
+#pragma unroll
+            for (int b = 0; b < R; ++b) {
+              if (NI == NJ && b > a) continue;
+              acc[m][a][b] = fmaf(xv.x, yv[b].x, acc[m][a][b]);
+              acc[m][a][b] = fmaf(xv.y, yv[b].y, acc[m][a][b]);
+              acc[m][a][b] = fmaf(xv.z, yv[b].z, acc[m][a][b]);
+              acc[m][a][b] = fmaf(xv.w, yv[b].w, acc[m][a][b]);
+            }
+          }
+      }
+#pragma unroll
+      for (int m = 0; m < M; ++m)
 #pragma unroll
         for (int a = 0; a < R; ++a)
 #pragma unroll
           for (int b = 0; b < R; ++b) {
-            acc[a][b] = fmaf(xv[a].x, yv[b].x, acc[a][b]);
-            acc[a][b] = fmaf(xv[a].y, yv[b].y, acc[a][b]);
-            acc[a][b] = fmaf(xv[a].z, yv[b].z, acc[a][b]);
-            acc[a][b] = fmaf(xv[a].w, yv[b].w, acc[a][b]);
+            const int i = ib + ti + NI * a, j = jb + tj + NJ * b;
+            if (i < TP && j <= i) f(m, i, j, acc[m][a][b]);
           }
-      }
-#pragma unroll
-      for (int a = 0; a < R; ++a)
-#pragma unroll
-        for (int b = 0; b < R; ++b) {
-          const int i = ib + ti + NI * a, j = jb + tj + NJ * b;
-          if (i < TP && j < TP) w[j * WP + i] = f(i, j, acc[a][b]);
-        }
     }
 }
 
 // Tiles that fit the tree: with few nodes a large tile is mostly its clamped
 // edge (13 nodes of 64 keys in 4 x 4 tiles: a third of the call).
-template <int DK, int NT, int QP, typename F>
-__device__ __forceinline__ void pair_products(const float* x, const float* y, float* w, int TP, int WP, F f) {
+template <int M, int DK, int NT, int QP, typename F>
+__device__ __forceinline__ void pair_products(const float* const (&x)[M], const float* y, int TP, F f) {
   if (TP <= 16)
-    pair_tiles<1, DK, NT, QP>(x, y, w, TP, WP, f);
+    pair_tiles<1, M, DK, NT, QP>(x, y, TP, f);
   else if (TP <= 32)
-    pair_tiles<2, DK, NT, QP>(x, y, w, TP, WP, f);
+    pair_tiles<2, M, DK, NT, QP>(x, y, TP, f);
   else
-    pair_tiles<4, DK, NT, QP>(x, y, w, TP, WP, f);
+    pair_tiles<4, M, DK, NT, QP>(x, y, TP, f);
 }
 
 template <int DK, int DV, typename T, bool kDelta>
@@ -163,38 +197,47 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
                  const int* __restrict__ count, T* __restrict__ out, int H, int ntok,
                  const float* __restrict__ alpha, float eps) {
   using Sh = TreeShape<DK, DV>;
-  constexpr int NT = Sh::NT, CG = Sh::CG, RG = Sh::RG, E = Sh::E, NW = Sh::NW, QP = Sh::QP;
+  constexpr int NT = Sh::NT, CG = Sh::CG, E = Sh::E, QP = Sh::QP;
   extern __shared__ __align__(16) float sm[];
   const long long bh = blockIdx.x;
   const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x;
   const int n = clamp_count(count, b, ntok);
   if (n == 0) return;
-  const TreeSmem<DK, DV, kDelta> L(n, ntok);
-  const int TP = L.TP, WP = L.WP, NB = L.nb;
+  const TreeSmem<DK, DV, kDelta> L(n);
+  const int TP = L.TP, WP = L.WP;
   float* fq = sm + L.q;
   float* fk = sm + L.k;
   float* vs = sm + L.v;
   float* wt = sm + L.w;
   float* qs = sm + L.qs;
-  float* part = sm + L.part;
   float* pw = sm + L.pw;
   int* depth = reinterpret_cast<int*>(sm + L.depth);
   int* up = reinterpret_cast<int*>(sm + L.up);
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(sm + L.mask);
 
-  // the state: thread (rg, cg) holds rows rg*E .. rg*E+E-1, columns 4cg .. 4cg+3
-  const int cg = tid % CG, rg = tid / CG;
+  // the state: column group cg, rows VE * (rl + RL * i) .. + VE - 1
+  constexpr int VE = E < 4 ? E : 4, EC = E / VE;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int rl = lane / Sh::CW, cgr = (warp % Sh::RW) * Sh::CW + lane % Sh::CW;
   const float4* Sb = reinterpret_cast<const float4*>(S + bh * (long long)DK * DV);
-  float4 s[E];
+  uint64_t s[E / 2][4];            // rows 2p and 2p + 1 of the lane's, four columns
 #pragma unroll
-  for (int e = 0; e < E; ++e) s[e] = Sb[(rg * E + e) * CG + cg];
+  for (int e = 0; e < E; e += 2) {
+    const float4* at = Sb + (VE * (rl + Sh::RL * (e / VE)) + e % VE) * CG + cgr;
+    const float4 x = at[0], y = at[CG];
+    s[e / 2][0] = pack2(x.x, y.x);
+    s[e / 2][1] = pack2(x.y, y.y);
+    s[e / 2][2] = pack2(x.z, y.z);
+    s[e / 2][3] = pack2(x.w, y.w);
+  }
 
   const T* qb = q + bh * (long long)ntok * DK;
   const T* kb = k + bh * (long long)ntok * DK;
   const T* vb = v + bh * (long long)ntok * DV;
   // rows, four values at a time, several loads of a thread in flight
   auto load_rows = [&](const T* src, int width, int pitch, float* dst, bool map) {
-    constexpr int U = 4;
+    // (large heads, 64 nodes: 285 us with four, 269 with eight; small ones lose)
+    constexpr int U = E >= 16 ? 8 : 4;
     const int per = width / 4, all = TP * per;
     for (int x0 = tid; x0 < all; x0 += U * NT) {
       float4 f[U];
@@ -226,97 +269,162 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
 
   // pair products under the ancestor mask
   if constexpr (kDelta) {
-    pair_products<DK, NT, QP>(fq, fk, wt, TP, WP, [&](int i, int j, float d) { return (mask[i] >> j) & 1 ? d : 0.f; });
-    pair_products<DK, NT, QP>(fk, fk, sm + L.w2, TP, WP,
-                              [&](int i, int j, float d) { return i != j && ((mask[i] >> j) & 1) ? d : 0.f; });
+    const float* x[2] = {fq, fk};
+    float* to[2] = {wt, sm + L.w2};
+    pair_products<2, DK, NT, QP>(x, fk, TP, [&](int m, int i, int j, float d) {
+      to[m][j * WP + i] = (m == 0 || i != j) && ((mask[i] >> j) & 1) ? d : 0.f;
+    });
   } else {
-    pair_products<DK, NT, QP>(fq, fk, wt, TP, WP, [&](int i, int j, float d) {
-      return (mask[i] >> j) & 1 ? d * pw[depth[i] - depth[j]] : 0.f;
+    const float* x[1] = {fq};
+    pair_products<1, DK, NT, QP>(x, fk, TP, [&](int, int i, int j, float d) {
+      wt[j * WP + i] = (mask[i] >> j) & 1 ? d * pw[depth[i] - depth[j]] : 0.f;
     });
   }
+  __syncthreads();
 
-  // the read: rows of x against the state, RG partial sums per node and column
+  // the read: rows of x against the state, G nodes at a time
   auto read_rows = [&](const float* x, auto put) {
-    for (int i0 = 0; i0 < n; i0 += NB) {
-      const int m = min(NB, n - i0);
-      __syncthreads();       // the previous group's partial sums have been read
-#pragma unroll 2
-      for (int i = 0; i < m; ++i) {
-        const float* row = x + (i0 + i) * QP + rg * E;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float xr[E];
-        if constexpr (E % 4 == 0) {
+    constexpr int G = Sh::G, RL = Sh::RL;
+    for (int i0 = (warp / Sh::RW) * G; i0 < n; i0 += Sh::SPLIT * G) {
+      uint64_t a2[4 * G] = {};
 #pragma unroll
-          for (int e = 0; e < E; e += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(row + e);
-            xr[e] = f.x; xr[e + 1] = f.y; xr[e + 2] = f.z; xr[e + 3] = f.w;
+      for (int ec = 0; ec < EC; ++ec)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float* row = x + min(i0 + g, n - 1) * QP + VE * (rl + RL * ec);
+          uint64_t xr[VE / 2];
+          if constexpr (VE == 4) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(row);
+            xr[0] = f.x;
+            xr[1] = f.y;
+          } else {
+            xr[0] = *reinterpret_cast<const uint64_t*>(row);
           }
-        } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) xr[e] = row[e];
-        }
+          for (int r = 0; r < VE / 2; ++r)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float c = xr[e];
-          acc.x = fmaf(c, s[e].x, acc.x);
-          acc.y = fmaf(c, s[e].y, acc.y);
-          acc.z = fmaf(c, s[e].z, acc.z);
-          acc.w = fmaf(c, s[e].w, acc.w);
+            for (int c = 0; c < 4; ++c) fma2(a2[4 * g + c], xr[r], s[ec * (VE / 2) + r][c]);
         }
-        // the row groups of a warp first
+      float a[4 * G];
 #pragma unroll
-        for (int o = CG; o < 32; o <<= 1) {
-          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
-          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
-          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
-          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
-        }
-        if ((tid & 31) < CG) *reinterpret_cast<float4*>(part + (i * NW + (tid >> 5)) * DV + 4 * cg) = acc;
+      for (int c = 0; c < 4 * G; ++c) a[c] = sum2(a2[c]);
+      // the sums over the warp's lanes: each exchange keeps one half
+#pragma unroll
+      for (int o = 16, h = 2 * G; o >= Sh::CW; o >>= 1, h >>= 1) {
+        const bool hi = (lane & o) != 0;
+#pragma unroll
+        for (int c = 0; c < 2 * G; ++c)
+          if (c < h) {
+            const float give = hi ? a[c] : a[c + h], keep = hi ? a[c + h] : a[c];
+            a[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
       }
-      __syncthreads();
-      for (int x2 = tid; x2 < m * DV; x2 += NT) {
-        const int i = x2 / DV, c = x2 % DV;
-        float t = 0.f;
+      constexpr int K = 4 * G / RL;            // values that a lane is left with
+      if constexpr (K >= 4) {
 #pragma unroll
-        for (int r = 0; r < NW; ++r) t += part[(i * NW + r) * DV + c];
-        put((i0 + i) * DV + c, t);
+        for (int c = 0; c < K; c += 4) {
+          const int i = i0 + (rl * K + c) / 4;
+          if (i < n) put(i * DV + 4 * cgr, make_float4(a[c], a[c + 1], a[c + 2], a[c + 3]));
+        }
+      } else {
+        const int i = i0 + rl * K / 4;
+        if (i < n)
+#pragma unroll
+          for (int c = 0; c < K; ++c) put(i * DV + 4 * cgr + (rl * K + c) % 4, a[c]);
       }
     }
   };
-  if constexpr (kDelta) read_rows(fk, [&](int at, float t) { vs[at] -= t; });   // v - S^T k
-  read_rows(fq, [&](int at, float t) { qs[at] = t; });
+  if constexpr (kDelta) {
+    read_rows(fk, [&](int at, auto t) { sub_from(vs + at, t); });                 // v - S^T k
+    __syncthreads();                                                              // the k rows' place is the result's
+  }
+  read_rows(fq, [&](int at, auto t) { *reinterpret_cast<decltype(t)*>(qs + at) = t; });
   __syncthreads();
 
   if constexpr (kDelta) {
-    // u_j over column c, one thread each: row j needs the rows on its path
+    // the increments in blocks of 8 rows: the paths before the block, a row's
+    // four columns per thread, then the rows of the block, a column per thread
+    // in registers (a column per thread all along took four to ten times as long)
     const float* at = sm + L.w2;
-    for (int c = tid; c < DV; c += NT)
-      for (int j = 0; j < n; ++j) {
-        float u = vs[j * DV + c];
-        for (unsigned long long m = mask[j] & ((1ull << j) - 1); m != 0ull; m &= m - 1) {
-          const int l = __ffsll((long long)m) - 1;
-          u = fmaf(-at[l * WP + j], vs[l * DV + c], u);
-        }
-        vs[j * DV + c] = u;
-      }
-    __syncthreads();
-  } else {
-    // 1 / den_i, one warp per node
-    for (int i = tid >> 5; i < n; i += NT / 32) {
-      float t = 0.f;
-      for (int r = tid & 31; r < DK; r += 32) t = fmaf(fq[i * QP + r], sm[L.z + r], t);
-      t *= pw[depth[i]];
-      for (int j = tid & 31; j <= i; j += 32) t += wt[j * WP + i];
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      const int j = j0 + tid / CG;
+      if (j0 > 0) {
+        if (tid < 8 * CG && j < n) {
+          float* to = vs + j * DV + 4 * (tid % CG);
+          float4 u = *reinterpret_cast<const float4*>(to);
+#pragma unroll 1
+          for (unsigned long long m = mask[j] & ((1ull << j0) - 1); m != 0ull;) {
+            constexpr int U = 4;             // rows' loads at a time
+            float p[U];
+            float4 x[U];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if ((tid & 31) == 0) sm[L.den + i] = 1.f / (t + eps);
+            for (int b = 0; b < U; ++b) {
+              const bool on = m != 0ull;
+              const int l = on ? __ffsll((long long)m) - 1 : 0;
+              m &= m - 1;
+              p[b] = on ? -at[l * WP + j] : 0.f;
+              x[b] = on ? *reinterpret_cast<const float4*>(vs + l * DV + 4 * (tid % CG)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int b = 0; b < U; ++b) {
+              u.x = fmaf(p[b], x[b].x, u.x);
+              u.y = fmaf(p[b], x[b].y, u.y);
+              u.z = fmaf(p[b], x[b].z, u.z);
+              u.w = fmaf(p[b], x[b].w, u.w);
+            }
+          }
+          *reinterpret_cast<float4*>(to) = u;
+        }
+        __syncthreads();
+      }
+      if (tid < DV) {
+        float u[8];
+        unsigned on[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int i = min(j0 + r, n - 1);
+          u[r] = vs[i * DV + tid];
+          on[r] = (unsigned)(mask[i] >> j0);
+        }
+#pragma unroll
+        for (int l = 0; l < 7; ++l) {
+          const float* row = at + min(j0 + l, n - 1) * WP + j0;
+          const float4 lo = *reinterpret_cast<const float4*>(row), hi = *reinterpret_cast<const float4*>(row + 4);
+          const float c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int r = l + 1; r < 8; ++r)
+            if ((on[r] >> l) & 1) u[r] = fmaf(-c[r], u[l], u[r]);
+        }
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (j0 + r < n) vs[(j0 + r) * DV + tid] = u[r];
+      }
+      __syncthreads();
+    }
+  } else {
+    // 1 / den_i, four lanes per node
+    for (int i0 = 0; i0 < n; i0 += NT / 4) {
+      const int i = min(i0 + tid / 4, n - 1), part = tid % 4;
+      float t = 0.f, u = 0.f;
+#pragma unroll 4
+      for (int r = 4 * part; r < DK; r += 16) {
+        const float4 x = *reinterpret_cast<const float4*>(fq + i * QP + r), y = *reinterpret_cast<const float4*>(sm + L.z + r);
+        t = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, t))));
+      }
+#pragma unroll 4
+      for (int j = part; j <= i; j += 4) u += wt[j * WP + i];
+      t = fmaf(t, pw[depth[i]], u);
+      t += __shfl_xor_sync(0xffffffffu, t, 1);
+      t += __shfl_xor_sync(0xffffffffu, t, 2);
+      if (part == 0) sm[L.den + i] = 1.f / (t + eps);
     }
     __syncthreads();
   }
 
   // out_i = (read + sum over the path) / den: 4 nodes x 4 columns per thread
   T* ob = out + bh * (long long)ntok * DV;
-  for (int i0 = 4 * rg; i0 < n; i0 += 4 * RG) {
+  const int cg = tid % CG;
+  for (int i0 = 4 * (tid / CG); i0 < n; i0 += 4 * Sh::RO) {
     float4 acc[4];
     unsigned long long m[4];
 #pragma unroll
@@ -358,20 +466,13 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   }
 }
 
-// The largest layout of any call (a call of 16 rows has the longer groups).
-template <int DK, int DV, bool kDelta>
-constexpr int tree_smem_most() {
-  const int a = TreeSmem<DK, DV, kDelta>(16, 16).total, b = TreeSmem<DK, DV, kDelta>(kTreeMax, kTreeMax).total;
-  return a > b ? a : b;
-}
-
 template <int DK, int DV, typename T, bool kDelta>
 cudaError_t launch(const TreeArgs& a) {
-  const int smem = TreeSmem<DK, DV, kDelta>(a.T, a.T).total * (int)sizeof(float);
+  const int smem = TreeSmem<DK, DV, kDelta>(a.T).total * (int)sizeof(float);
   auto kern = tree_simt_kernel<DK, DV, T, kDelta>;
   static KernelOnce once;
   int resident = 0;
-  constexpr int most = tree_smem_most<DK, DV, kDelta>() * (int)sizeof(float);
+  constexpr int most = TreeSmem<DK, DV, kDelta>(kTreeMax).total * (int)sizeof(float);
   static_assert(most <= 232448, "shared memory budget");
   cudaError_t e = once.prepare(kern, TreeShape<DK, DV>::NT, most, &resident);
   if (e != cudaSuccess) return e;
