@@ -197,7 +197,10 @@ struct Part {
 
 // This warp's sum of the weights of tokens [t0, t1). vec: every row starts on
 // a 16-byte boundary (t0 and t1 are multiples of a load then, or t1 = V is).
-template <typename T>
+// Rows that start anywhere are read a value at a time, US loads in flight: 16
+// for the tree (25.3 us for the trees below with 8, 24.0 with 16), 8 for the
+// chain, which reads two rows and loses with the registers (17.2 and 17.9).
+template <int US, typename T>
 __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
   const int lane = threadIdx.x & 31;
   float hi = 0.f, lo = 0.f;
@@ -236,7 +239,7 @@ __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
         }
     }
   } else {
-    constexpr int U = 8;
+    constexpr int U = US;
     for (int tb = t0 + lane; tb < t1; tb += U * 32) {
       float x[U], y[U];
 #pragma unroll
@@ -256,11 +259,11 @@ __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
 }
 
 // The sums of all warps' parts of a row, in every CTA (one cluster barrier).
-template <typename T>
+template <int US, typename T>
 __device__ void row_sums(const T* p, const T* q, int V, bool vec, int rank, int nc, VerifyShared& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Part part(V, rank, nc, warp);
-  const Pair x = span_total(p, q, part.w0, part.w1, vec);
+  const Pair x = span_total<US>(p, q, part.w0, part.w1, vec);
   if (lane < nc) peer_store(peer(&sh.sums[rank * VW + warp], lane), x);
   __syncwarp();
   cluster_sync();
@@ -335,7 +338,7 @@ __device__ int draw(const T* p, const T* q, int V, const Found& f, int rank, int
     upto = prefix<32>(x);
     sum = from_lane(upto, 31);
   } else {
-    sum = span_total(p, q, t0, t1, false);
+    sum = span_total<8>(p, q, t0, t1, false);
   }
   if (lane == 0) sh.sub_sum[warp] = sum;
   __syncthreads();
@@ -383,6 +386,29 @@ __device__ int draw(const T* p, const T* q, int V, const Found& f, int rank, int
   return sh.found;
 }
 
+// This CTA's part of the rows of the first four children of context `at` into
+// L2, one warp each, while the first warp searches: the row that comes next is
+// then mostly there (24.0 -> 23 us; one child 24.0, fifteen 23.4). Only where
+// few sequences leave HBM idle, since rows that are not needed come along.
+template <typename T>
+__device__ __forceinline__ void prefetch_children(const T* pb, int at, int all, int V, int rank, int nc,
+                                                  const VerifyShared& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < 1 || warp > 4) return;
+  unsigned long long m = 0ull;
+  for (int i0 = 0; i0 < all; i0 += 32) {
+    const int i = i0 + lane;
+    m |= (unsigned long long)__ballot_sync(0xffffffffu, i < all && i > at && sh.par[i] == at) << i0;
+  }
+  for (int i = 1; i < warp; ++i) m &= m - 1;
+  if (m == 0ull) return;
+  const T* row = pb + (long long)__ffsll((long long)m) * V;        // child c has row c + 1
+  constexpr int kLine = 128 / sizeof(T);
+  const int t1 = Part(V, rank, nc, VW - 1).w1;
+  for (int t = Part(V, rank, nc, 0).w0 + lane * kLine; t < t1; t += 32 * kLine)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + t));
+}
+
 // A total that can be drawn from (an infinite weight makes it no number).
 __device__ __forceinline__ bool drawable(Pair total) { return total.h > 0.f && total.h <= 3.4e38f; }
 
@@ -414,13 +440,13 @@ chain_kernel(const T* __restrict__ target, const T* __restrict__ draft, const in
   const T* p = pb + (long long)n * V;
   const T* q = n < all ? qb + (long long)n * V : nullptr;
   cluster_wait();
-  row_sums(p, q, V, vec, rank, nc, sh);
+  row_sums<8>(p, q, V, vec, rank, nc, sh);
   Found f = find_part(sh, nc, u);
   if (!(f.total.h > 0.f)) {
     // nothing left to draw from (p <= q everywhere): from p itself
     cluster_sync();                            // the sums have been read
     q = nullptr;
-    row_sums(p, q, V, vec, rank, nc, sh);
+    row_sums<8>(p, q, V, vec, rank, nc, sh);
     f = find_part(sh, nc, u);
   }
   const bool some = drawable(f.total);
@@ -452,7 +478,8 @@ tree_verify_kernel(const T* __restrict__ target, const int* __restrict__ tokens,
   for (int step = 0; step <= ntok; ++step) {
     const T* p = pb + (long long)(at + 1) * V;
     const float u = uniform[(long long)b * (ntok + 1) + at + 1];
-    row_sums<T>(p, nullptr, V, vec, rank, nc, sh);
+    row_sums<16, T>(p, nullptr, V, vec, rank, nc, sh);
+    if (nc == kMaxCluster) prefetch_children(pb, at, all, V, rank, nc, sh);
     const Found f = find_part(sh, nc, u);
     token = -1;
     int child = -1;
