@@ -16,7 +16,7 @@
 // 128 states, three quarters of the issue slots. Packing, a lane takes eight
 // consecutive values, so that four lanes (two for dv = 16) share a block and
 // two shuffles join its maximum; infinities are looked for only where the
-// maximum is one: 26.4 us, 0.95 of the floor. Unpacking, a lane takes four
+// maximum is one: 26.7 us, 0.94 of the floor. Unpacking, a lane takes four
 // values, so that a warp's stores are whole lines (30 us for 2048 states, four
 // bytes written for each one read). Four loads of a lane are in flight.
 #include <cuda_fp8.h>

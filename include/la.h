@@ -329,7 +329,7 @@ LA_API la_status la_state_copy(float* dst_S, float* dst_z, const float* src_S,
  * checked against the target's probabilities (la_verify_chain,
  * la_verify_tree), and the state moves along the ones that stand
  * (la_state_advance). None of the calls needs a workspace, keeps anything
- * between calls or uses atomics: results repeat bit for bit, and calls on
+ * between calls or joins results by atomics: results repeat bit for bit, and calls on
  * different streams do not meet. int arrays are device memory, 4-byte
  * aligned; what they hold cannot be checked without waiting for the GPU, so
  * each entry point says what an entry out of range does (no access leaves the
