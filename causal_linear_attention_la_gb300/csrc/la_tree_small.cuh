@@ -4,14 +4,15 @@
 // With few nodes the call is bound by the state's way to the products: one 64
 // KiB read a head, of which the lanes' own fragment loads reach L1 in 64-byte
 // pieces, two wavefronts each (47 us for 16 nodes on 2048 d = 128 states, L1
-// at half of its rate, 11000 cycles a CTA). Here the state comes as bulk
-// copies, a row each, into shared memory whose row pitch is a multiple of 128
-// bytes plus 16, so that a fragment's four rows lie in different banks; the
-// copies run while q, k and v are prepared, and the CTA that takes this one's
-// place finds its state and rows in L2.
+// at half of its rate, 11000 cycles a CTA). Here the whole state comes by TMA,
+// in boxes of 32 columns with the 128-byte swizzle, so that a fragment's rows
+// lie in different banks (row by row as bulk copies of 512 bytes: 60 cycles of
+// issue each, 52 us); the boxes are under way while q, k and v are prepared. 16
+// nodes on 2048 states take 30 us, 0.82 of what HBM allows.
 //
-// One CTA per (batch, head): one warp per 16 value columns and one more that
-// issues the copies and works out the ancestor masks. Three
+// One CTA per (batch, head), two per SM at d = 128: one warp per 16 value
+// columns and one more that starts the copies and works out the ancestor
+// masks; an SM's two CTAs start apart. Three
 // barriers:
 //   rows    phi(q), phi(k) as bf16 hi and lo, v, phi(q).z
 //   pairs   every warp a 16 x 16 product over its own keys (K split over the
@@ -106,7 +107,7 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
   int odd_values = 0;
 
   if (warp == NW) {
-    // ---- the state's rows, the tree, what the next CTA needs
+    // ---- the state's boxes, the tree
     if (lane == 0) {
       sm100::mbar_init(bar, 1);
       sm100::fence_mbar_init();
