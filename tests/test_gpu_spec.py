@@ -144,6 +144,30 @@ def test_tree_sizes_on_tensor_cores(dk, dv, rule):
 
 
 @pytest.mark.parametrize("rule", ["plain", "decay", "delta"])
+@pytest.mark.parametrize("dv", [16, 32, 64, 128])
+@pytest.mark.parametrize("dk", [16, 32, 64, 128])
+def test_tree_sizes_on_cuda_cores(dk, dv, rule):
+    """Every head size of the CUDA-core kernel, both sides of its node groups
+    (4 or 8), of the delta rule's blocks (8) and of its pair tiles (16, 32)."""
+    H = 2
+    delta = rule == "delta"
+    alpha = np.array([0.7, 0.95], np.float32) if rule == "decay" else None
+    for T in (1, 3, 4, 5, 8, 9, 16, 17, 32, 33, 64):
+        B = 3
+        S, z = state(B, H, dk, dv, T, delta)
+        q, k, v = rows(B, H, T, dk, dv, T + 1, "f32", delta)
+        parent = np.stack([np.arange(T) - 1, np.full(T, -1), tree(1, T, T)[0]])
+        args = [to_dev(x, "f32") for x in (q, k, v)] + [i32(parent)]
+        if delta:
+            out = la.decode_tree_delta(cuda(S), *args)
+            want, scale = spec.decode_tree_delta(S, q, k, v, parent)
+        else:
+            out = la.decode_tree(cuda(S), cuda(z), *args, alpha=None if alpha is None else cuda(alpha))
+            want, scale = spec.decode_tree(S, z, q, k, v, parent, alpha)
+        near(to_host(out), want, scale, "f32", gamma(dk, T if delta else 1))
+
+
+@pytest.mark.parametrize("rule", ["plain", "decay", "delta"])
 def test_tree_of_64_ragged(rule):
     """Trees of every size class in one call of 64 rows; rows behind them stay."""
     B, H, T, d = 10, 2, 64, 128
