@@ -719,7 +719,7 @@ def decode_tree(S, z, q, k, v, parent, alpha=None, eps=1e-6, count=None, out=Non
     dev, f32, i32 = S.get_device(), torch.float32, torch.int32
     code = _dtype_code(q)
     if out is None:
-        out = (torch.empty if count is None else torch.zeros)((B, H, T, dv), dtype=q.dtype, device=S.device)
+        out = (torch.empty_like if count is None else torch.zeros_like)(v)      # (v is checked with the others)
     _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("z", z, f32, (B, H, dk)), ("q", q, q.dtype, (B, H, T, dk)),
                ("k", k, q.dtype, (B, H, T, dk)), ("v", v, q.dtype, (B, H, T, dv)), ("parent", parent, i32, (B, T)),
                ("alpha", alpha, f32, (H,)), ("count", count, i32, (B,)), ("out", out, q.dtype, (B, H, T, dv)))
@@ -737,7 +737,7 @@ def decode_tree_delta(S, q, k, v, parent, count=None, out=None):
     dev, f32, i32 = S.get_device(), torch.float32, torch.int32
     code = _dtype_code(q)
     if out is None:
-        out = (torch.empty if count is None else torch.zeros)((B, H, T, dv), dtype=q.dtype, device=S.device)
+        out = (torch.empty_like if count is None else torch.zeros_like)(v)      # (v is checked with the others)
     _need_like(dev, ("S", S, f32, (B, H, dk, dv)), ("q", q, q.dtype, (B, H, T, dk)), ("k", k, q.dtype, (B, H, T, dk)),
                ("v", v, q.dtype, (B, H, T, dv)), ("parent", parent, i32, (B, T)), ("count", count, i32, (B,)),
                ("out", out, q.dtype, (B, H, T, dv)))
@@ -774,7 +774,7 @@ def verify_tree(target, tokens, parent, uniform, count=None):
     code = _dtype_code(target)
     _need_like(dev, ("target", target, target.dtype, (B, T + 1, V)), ("tokens", tokens, i32, (B, T)),
                ("parent", parent, i32, (B, T)), ("uniform", uniform, torch.float32, (B, T + 1)), ("count", count, i32, (B,)))
-    path = torch.empty((B, T), dtype=i32, device=target.device)
+    path = torch.empty_like(tokens)
     accepted = torch.empty((B,), dtype=i32, device=target.device)
     nxt = torch.empty((B,), dtype=i32, device=target.device)
     _on(dev, lib().la_verify_tree, target.data_ptr(), tokens.data_ptr(), parent.data_ptr(), _ptr(count),

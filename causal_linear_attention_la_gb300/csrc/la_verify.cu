@@ -23,7 +23,7 @@
 // One thread-block cluster per sequence: each CTA takes a contiguous part of
 // the vocabulary, each warp a contiguous part of that, so that the joined
 // sums are prefix sums in token order. Every warp sends its sum to all CTAs
-// (distributed shared memory), every warp finds the part that holds the answer
+// (distributed shared memory), one warp of each finds the part that holds the answer
 // by one scan over all of them; the CTA that has it splits it over its warps
 // again and scans the last piece. (Sums joined per CTA first, and added up one
 // after the other, took as long as the rows: 31 us for the trees below.)
