@@ -22,9 +22,10 @@
 // small trees are bound by the chain of these steps, large ones by the read's
 // shared-memory loads and exchanges (d = 128: 20 cycles a warp and node against
 // 16 for its arithmetic) with the few warps that the registers leave.
-// 1536 fp32 states: 64 nodes at d = 128 269 us, with the delta rule 387 (350 and
-// 668 with the read's sums met in shared memory and one thread per column in the
-// delta rule's solve); at d = 64 95 and 179 (152 and 348).
+// 1536 fp32 states: 64 nodes at d = 128 197 us, with the delta rule 381 (350 and
+// 668 with the read's sums met in shared memory, v beside q and k throughout and
+// one thread per column in the delta rule's solve); at d = 64 95 and 163 (152
+// and 348).
 #include "la_tree.cuh"
 
 namespace la {
@@ -48,29 +49,31 @@ struct TreeShape {
   static constexpr int G = RL > 16 ? 8 : 4;                      // nodes at a time
   // CTAs per SM that the registers are cut for: two where a thread holds 64 of
   // them for the state; four of 256 threads (1536 fp32 states at d = 64 with four
-  // and three: 16 nodes 32 and 39 us, 24 45 and 52, 64 with the delta rule 179
-  // and 171); six of 128 (d = 32, bf16, with eight and six: 16 nodes 20 and 18,
-  // 64 with the delta rule 102 and 93)
+  // and three: 16 nodes 32 and 39 us, 24 45 and 52); six of 128 (d = 32, bf16, with
+  // eight and six: 16 nodes 20 and 18, 64 with the delta rule 102 and 93)
   static constexpr int CTAS = E >= 16 ? 2 : NT == 128 ? 6 : 1024 / NT;
   static_assert(RL <= 32 && CW >= 1 && RW * CW == CG && SPLIT >= 1 && SPLIT * RW * 32 == NT, "read layout");
 };
 
 // Shared-memory layout in floats for T nodes. The read's result takes the place
-// of the k rows, which are done with by then, where its rows fit.
+// of the k rows, which are done with by then, where its rows fit. The delta
+// rule's key products, strictly below the diagonal, are the other triangle of
+// the weights (in an array of their own: 56 nodes on 1536 d = 128 states 350 us,
+// now 282). late: v comes after the read, where q (and k) were.
 template <int DK, int DV, bool kDelta>
 struct TreeSmem {
-  int TP, WP, q, k, v, w, w2, qs, z, den, pw, depth, mask, up, total;
-  __host__ __device__ constexpr explicit TreeSmem(int T)
-      : TP(0), WP(0), q(0), k(0), v(0), w(0), w2(0), qs(0), z(0), den(0), pw(0), depth(0), mask(0), up(0), total(0) {
+  int TP, WP, q, k, v, w, qs, z, den, pw, depth, mask, up, total;
+  __host__ __device__ constexpr TreeSmem(int T, bool late)
+      : TP(0), WP(0), q(0), k(0), v(0), w(0), qs(0), z(0), den(0), pw(0), depth(0), mask(0), up(0), total(0) {
     using Sh = TreeShape<DK, DV>;
     TP = (T + 3) & ~3;
     WP = TP + 4;
     q = 0;
     k = q + TP * Sh::QP;
-    v = k + TP * Sh::QP;
-    w = v + TP * DV;
-    w2 = w + TP * WP;
-    z = w2 + (kDelta ? TP * WP : 0);
+    w = k + TP * Sh::QP;
+    v = late ? q : w;
+    w += late ? 0 : TP * DV;
+    z = w + TP * WP;
     qs = DV <= Sh::QP ? k : z + DK;
     den = z + DK + (DV <= Sh::QP ? 0 : TP * DV);
     pw = den + TP;
@@ -79,6 +82,18 @@ struct TreeSmem {
     mask = up + TP;                 // 8-byte entries
     mask = (mask + 1) & ~1;
     total = mask + 2 * TP;
+  }
+  // v late where only that lets two CTAs share an SM (228 KiB, 1 KiB of it taken
+  // by each CTA): 1536 states of 64 nodes at d = 128 269 us without, 197 with
+  static constexpr int kHalf = 116736 - 1024;
+  __host__ __device__ static constexpr bool late(int T) {
+    return !kDelta && DV <= 2 * TreeShape<DK, DV>::QP && TreeSmem(T, false).total * 4 > kHalf;
+  }
+  static constexpr int bytes(int T) { return TreeSmem(T, late(T)).total * 4; }
+  static constexpr int most() {
+    int m = 0;
+    for (int t = 1; t <= kTreeMax; ++t) m = bytes(t) > m ? bytes(t) : m;
+    return m;
   }
 };
 
@@ -203,7 +218,9 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x;
   const int n = clamp_count(count, b, ntok);
   if (n == 0) return;
-  const TreeSmem<DK, DV, kDelta> L(n);
+  using Smem = TreeSmem<DK, DV, kDelta>;
+  const bool late = Smem::late(kTreeMax) && Smem::late(ntok);      // (the first is known when compiled)
+  const Smem L(n, late);
   const int TP = L.TP, WP = L.WP;
   float* fq = sm + L.q;
   float* fk = sm + L.k;
@@ -236,7 +253,7 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   const T* vb = v + bh * (long long)ntok * DV;
   // rows, four values at a time, several loads of a thread in flight
   auto load_rows = [&](const T* src, int width, int pitch, float* dst, bool map) {
-    // (large heads, 64 nodes: 285 us with four, 269 with eight; small ones lose)
+    // (d = 128, 64 nodes: 285 us with four, 269 with eight; small heads lose)
     constexpr int U = E >= 16 ? 8 : 4;
     const int per = width / 4, all = TP * per;
     for (int x0 = tid; x0 < all; x0 += U * NT) {
@@ -259,7 +276,12 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   if (tid >= NT - 32) tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, up);
   load_rows(qb, DK, QP, fq, !kDelta);
   load_rows(kb, DK, QP, fk, !kDelta);
-  load_rows(vb, DV, DV, vs, false);
+  if (!late) {
+    load_rows(vb, DV, DV, vs, false);
+  } else {
+    constexpr int kLine = 128 / sizeof(T);
+    for (int x = tid * kLine; x < n * DV; x += NT * kLine) asm volatile("prefetch.global.L2 [%0];" ::"l"(vb + x));
+  }
   if (!kDelta) {
     for (int r = tid; r < DK; r += NT) sm[L.z + r] = z[bh * DK + r];
     const float a = alpha != nullptr ? alpha[h] : 1.f;
@@ -270,9 +292,8 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
   // pair products under the ancestor mask
   if constexpr (kDelta) {
     const float* x[2] = {fq, fk};
-    float* to[2] = {wt, sm + L.w2};
     pair_products<2, DK, NT, QP>(x, fk, TP, [&](int m, int i, int j, float d) {
-      to[m][j * WP + i] = (m == 0 || i != j) && ((mask[i] >> j) & 1) ? d : 0.f;
+      if (m == 0 || i != j) wt[m == 0 ? j * WP + i : i * WP + j] = (mask[i] >> j) & 1 ? d : 0.f;
     });
   } else {
     const float* x[1] = {fq};
@@ -281,6 +302,25 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
     });
   }
   __syncthreads();
+
+  if constexpr (!kDelta) {
+    // 1 / den_i, four lanes per node
+    for (int i0 = 0; i0 < n; i0 += NT / 4) {
+      const int i = min(i0 + tid / 4, n - 1), part = tid % 4;
+      float t = 0.f, u = 0.f;
+#pragma unroll 4
+      for (int r = 4 * part; r < DK; r += 16) {
+        const float4 x = *reinterpret_cast<const float4*>(fq + i * QP + r), y = *reinterpret_cast<const float4*>(sm + L.z + r);
+        t = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, t))));
+      }
+#pragma unroll 4
+      for (int j = part; j <= i; j += 4) u += wt[j * WP + i];
+      t = fmaf(t, pw[depth[i]], u);
+      t += __shfl_xor_sync(0xffffffffu, t, 1);
+      t += __shfl_xor_sync(0xffffffffu, t, 2);
+      if (part == 0) sm[L.den + i] = 1.f / (t + eps);
+    }
+  }
 
   // the read: rows of x against the state, G nodes at a time
   auto read_rows = [&](const float* x, auto put) {
@@ -345,7 +385,6 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
     // the increments in blocks of 8 rows: the paths before the block, a row's
     // four columns per thread, then the rows of the block, a column per thread
     // in registers (a column per thread all along took four to ten times as long)
-    const float* at = sm + L.w2;
     for (int j0 = 0; j0 < n; j0 += 8) {
       const int j = j0 + tid / CG;
       if (j0 > 0) {
@@ -362,7 +401,7 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
               const bool on = m != 0ull;
               const int l = on ? __ffsll((long long)m) - 1 : 0;
               m &= m - 1;
-              p[b] = on ? -at[l * WP + j] : 0.f;
+              p[b] = on ? -wt[j * WP + l] : 0.f;
               x[b] = on ? *reinterpret_cast<const float4*>(vs + l * DV + 4 * (tid % CG)) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
@@ -379,21 +418,16 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
       }
       if (tid < DV) {
         float u[8];
-        unsigned on[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const int i = min(j0 + r, n - 1);
           u[r] = vs[i * DV + tid];
-          on[r] = (unsigned)(mask[i] >> j0);
-        }
-#pragma unroll
-        for (int l = 0; l < 7; ++l) {
-          const float* row = at + min(j0 + l, n - 1) * WP + j0;
-          const float4 lo = *reinterpret_cast<const float4*>(row), hi = *reinterpret_cast<const float4*>(row + 4);
+          const unsigned on = (unsigned)(mask[i] >> j0);
+          const float4 lo = *reinterpret_cast<const float4*>(wt + i * WP + j0), hi = *reinterpret_cast<const float4*>(wt + i * WP + j0 + 4);
           const float c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int r = l + 1; r < 8; ++r)
-            if ((on[r] >> l) & 1) u[r] = fmaf(-c[r], u[l], u[r]);
+          for (int l = 0; l < r; ++l)
+            if ((on >> l) & 1) u[r] = fmaf(-c[l], u[l], u[r]);
         }
 #pragma unroll
         for (int r = 1; r < 8; ++r)
@@ -401,23 +435,8 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
       }
       __syncthreads();
     }
-  } else {
-    // 1 / den_i, four lanes per node
-    for (int i0 = 0; i0 < n; i0 += NT / 4) {
-      const int i = min(i0 + tid / 4, n - 1), part = tid % 4;
-      float t = 0.f, u = 0.f;
-#pragma unroll 4
-      for (int r = 4 * part; r < DK; r += 16) {
-        const float4 x = *reinterpret_cast<const float4*>(fq + i * QP + r), y = *reinterpret_cast<const float4*>(sm + L.z + r);
-        t = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, t))));
-      }
-#pragma unroll 4
-      for (int j = part; j <= i; j += 4) u += wt[j * WP + i];
-      t = fmaf(t, pw[depth[i]], u);
-      t += __shfl_xor_sync(0xffffffffu, t, 1);
-      t += __shfl_xor_sync(0xffffffffu, t, 2);
-      if (part == 0) sm[L.den + i] = 1.f / (t + eps);
-    }
+  } else if (late) {
+    load_rows(vb, DV, DV, vs, false);
     __syncthreads();
   }
 
@@ -468,11 +487,11 @@ tree_simt_kernel(const float* __restrict__ S, const float* __restrict__ z, const
 
 template <int DK, int DV, typename T, bool kDelta>
 cudaError_t launch(const TreeArgs& a) {
-  const int smem = TreeSmem<DK, DV, kDelta>(a.T).total * (int)sizeof(float);
+  const int smem = TreeSmem<DK, DV, kDelta>::bytes(a.T);
   auto kern = tree_simt_kernel<DK, DV, T, kDelta>;
   static KernelOnce once;
   int resident = 0;
-  constexpr int most = TreeSmem<DK, DV, kDelta>(kTreeMax).total * (int)sizeof(float);
+  constexpr int most = TreeSmem<DK, DV, kDelta>::most();
   static_assert(most <= 232448, "shared memory budget");
   cudaError_t e = once.prepare(kern, TreeShape<DK, DV>::NT, most, &resident);
   if (e != cudaSuccess) return e;

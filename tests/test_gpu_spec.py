@@ -193,6 +193,33 @@ def test_tree_of_64_ragged(rule):
         near(got[b, :, :n], want[b, :, :n], scale[b, :, :n], "bf16", gamma(d, T if delta else 1, True))
 
 
+@pytest.mark.parametrize("rule", ["plain", "decay", "delta"])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128), (128, 64), (32, 128)])
+def test_tree_of_64_ragged_f32(dk, dv, rule):
+    """The same on the CUDA cores, whose layout goes by the rows of the call."""
+    B, H, T = 9, 2, 64
+    delta = rule == "delta"
+    count = [0, 1, 7, 16, 31, 33, 59, 61, 64]
+    alpha = np.array([0.5, 1.0], np.float32) if rule == "decay" else None
+    S, z = state(B, H, dk, dv, 47, delta)
+    q, k, v = rows(B, H, T, dk, dv, 48, "f32", delta)
+    for b, n in enumerate(count):
+        q[b, :, n:], k[b, :, n:], v[b, :, n:] = np.nan, np.inf, np.nan
+    parent = tree(B, T, 49, lean=0.2)
+    args = [to_dev(x, "f32") for x in (q, k, v)] + [i32(parent)]
+    out = to_dev(np.full((B, H, T, dv), -3.0, np.float32), "f32")
+    if delta:
+        la.decode_tree_delta(cuda(S), *args, count=i32(count), out=out)
+        want, scale = spec.decode_tree_delta(S, q, k, v, parent, count)
+    else:
+        la.decode_tree(cuda(S), cuda(z), *args, alpha=None if alpha is None else cuda(alpha), count=i32(count), out=out)
+        want, scale = spec.decode_tree(S, z, q, k, v, parent, alpha, count)
+    got = to_host(out)
+    for b, n in enumerate(count):
+        assert np.all(got[b, :, n:] == -3.0)
+        near(got[b, :, :n], want[b, :, :n], scale[b, :, :n], "f32", gamma(dk, T if delta else 1))
+
+
 def test_tree_repeats_bit_for_bit():
     import torch
     B, H, T, d = 40, 8, 40, 128
