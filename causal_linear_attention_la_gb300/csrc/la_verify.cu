@@ -200,6 +200,8 @@ struct Part {
 // Rows that start anywhere are read a value at a time, US loads in flight: 16
 // for the tree (25.3 us for the trees below with 8, 24.0 with 16), 8 for the
 // chain, which reads two rows and loses with the registers (17.2 and 17.9).
+// (The children's rows brought into L2 during the search: a captured sequence
+// of calls 24.0 -> 23.3 us, a call by itself 24.6 -> 26.6. Left out.)
 template <int US, typename T>
 __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
   const int lane = threadIdx.x & 31;
@@ -386,29 +388,6 @@ __device__ int draw(const T* p, const T* q, int V, const Found& f, int rank, int
   return sh.found;
 }
 
-// This CTA's part of the rows of the first four children of context `at` into
-// L2, one warp each, while the first warp searches: the row that comes next is
-// then mostly there (24.0 -> 23 us; one child 24.0, fifteen 23.4). Only where
-// few sequences leave HBM idle, since rows that are not needed come along.
-template <typename T>
-__device__ __forceinline__ void prefetch_children(const T* pb, int at, int all, int V, int rank, int nc,
-                                                  const VerifyShared& sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < 1 || warp > 4) return;
-  unsigned long long m = 0ull;
-  for (int i0 = 0; i0 < all; i0 += 32) {
-    const int i = i0 + lane;
-    m |= (unsigned long long)__ballot_sync(0xffffffffu, i < all && i > at && sh.par[i] == at) << i0;
-  }
-  for (int i = 1; i < warp; ++i) m &= m - 1;
-  if (m == 0ull) return;
-  const T* row = pb + (long long)__ffsll((long long)m) * V;        // child c has row c + 1
-  constexpr int kLine = 128 / sizeof(T);
-  const int t1 = Part(V, rank, nc, VW - 1).w1;
-  for (int t = Part(V, rank, nc, 0).w0 + lane * kLine; t < t1; t += 32 * kLine)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + t));
-}
-
 // A total that can be drawn from (an infinite weight makes it no number).
 __device__ __forceinline__ bool drawable(Pair total) { return total.h > 0.f && total.h <= 3.4e38f; }
 
@@ -479,7 +458,6 @@ tree_verify_kernel(const T* __restrict__ target, const int* __restrict__ tokens,
     const T* p = pb + (long long)(at + 1) * V;
     const float u = uniform[(long long)b * (ntok + 1) + at + 1];
     row_sums<16, T>(p, nullptr, V, vec, rank, nc, sh);
-    if (nc == kMaxCluster) prefetch_children(pb, at, all, V, rank, nc, sh);
     const Found f = find_part(sh, nc, u);
     token = -1;
     int child = -1;
