@@ -30,7 +30,8 @@ __all__ = [
     "la_forward_workspace_size", "la_backward_workspace_size",
     "la_set_path", "la_forward_path", "la_backward_path", "la_decode_path",
     "la_profile_enable", "la_profile_read", "la_launch_count", "SPAN_NAMES",
-    "la_device_status", "la_test_timeout_next_forward", "la_forward_noalloc", "LA_NOALLOC_SCRATCH_BYTES",
+    "la_device_status", "la_test_timeout_next_forward", "la_test_timeout_next_tree",
+    "la_forward_noalloc", "LA_NOALLOC_SCRATCH_BYTES",
     "la_forward_host", "la_forward_host_workspace_size", "forward_host",
     "la_backward_saved", "backward_saved", "la_backward_decay", "backward_decay",
     "forward", "decode_step", "decode_steps", "backward",
@@ -58,7 +59,7 @@ exported_symbols = (
     "la_backward_workspace_size", "la_backward",
     "la_set_path", "la_forward_path", "la_backward_path", "la_decode_path",
     "la_profile_enable", "la_profile_read", "la_launch_count",
-    "la_device_status", "la_test_timeout_next_forward", "la_forward_noalloc",
+    "la_device_status", "la_test_timeout_next_forward", "la_test_timeout_next_tree", "la_forward_noalloc",
     "la_forward_host_workspace_size", "la_forward_host", "la_backward_saved",
     "la_backward_decay", "la_forward_delta", "la_forward_plan",
     "la_decode_tree", "la_decode_tree_delta", "la_tree_path", "la_verify_chain", "la_verify_tree",
@@ -165,6 +166,8 @@ def lib():
     h.la_device_status.argtypes = [_c_int]
     h.la_test_timeout_next_forward.restype = None
     h.la_test_timeout_next_forward.argtypes = []
+    h.la_test_timeout_next_tree.restype = None
+    h.la_test_timeout_next_tree.argtypes = []
     h.la_forward_noalloc.restype = _c_int
     h.la_forward_noalloc.argtypes = ([_c_void] * 4 + [_c_int] * 6 + [_c_float, _c_int]
                                      + [_c_void, _c_void, _c_void])
@@ -343,6 +346,10 @@ def la_device_status(clear=False):
 
 def la_test_timeout_next_forward():
     lib().la_test_timeout_next_forward()
+
+
+def la_test_timeout_next_tree():
+    lib().la_test_timeout_next_tree()
 
 
 def la_profile_enable(on):

@@ -60,6 +60,10 @@ cudaError_t verify(const VerifyArgs& a);
 cudaError_t state_pack(const PackArgs& a);
 cudaError_t state_unpack(const PackArgs& a);
 
+// One-shot test switch (la_test_timeout_next_tree): true once after the
+// switch has been set.
+bool take_tree_timeout_test();
+
 // The current la_set_path setting.
 int current_path();
 

@@ -5,6 +5,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "la_spec.cuh"
 
 namespace la {
@@ -117,7 +119,14 @@ la_status pack_call(const char* who, const PackArgs& a, bool pack) {
   return e == cudaSuccess ? LA_OK : cuda_fail(e, who);
 }
 
+std::atomic<int> g_tree_timeout_test{0};
+
 }  // namespace
+
+bool take_tree_timeout_test() {
+  return g_tree_timeout_test.load(std::memory_order_relaxed) != 0 && g_tree_timeout_test.exchange(0) != 0;
+}
+
 }  // namespace la
 
 using namespace la;
@@ -128,6 +137,8 @@ int la_tree_path(int dk, int dv, la_dtype dtype) {
   if (!head_ok(dk) || !head_ok(dv) || (dtype != LA_F32 && dtype != LA_BF16)) return -1;
   return current_path() == LA_PATH_AUTO && tree_on_tensor_cores(dk, dv, dtype) ? 1 : 0;
 }
+
+void la_test_timeout_next_tree(void) { la::g_tree_timeout_test.store(1); }
 
 la_status la_decode_tree(const float* S, const float* z, const void* q, const void* k, const void* v,
                          const int* parent, const int* count, void* out, int B, int H, int T, int dk, int dv,

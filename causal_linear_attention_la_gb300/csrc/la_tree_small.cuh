@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(2 * DV + 32, DV == 128 ? 2 : 4)
 tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restrict__ S, const float* __restrict__ z, const __nv_bfloat16* __restrict__ q,
                   const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                   const int* __restrict__ parent, const int* __restrict__ count, __nv_bfloat16* __restrict__ out, int H,
-                  int ntok, const float* __restrict__ alpha, float eps, int* status, unsigned late0, unsigned late1) {
+                  int ntok, const float* __restrict__ alpha, float eps, int* status, int stall, unsigned late0,
+                  unsigned late1) {
   using L = Small<DK, DV, kDelta>;
   constexpr int NT = L::NT, NW = L::NW, KS = L::KS, KW = L::KW, BOX = L::BOX, QP = L::QP, VP = L::VP;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -111,7 +112,8 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
     if (lane == 0) {
       sm100::mbar_init(bar, 1);
       sm100::fence_mbar_init();
-      sm100::mbar_arrive_expect_tx(bar, DK * DV * 4);
+      // (stall, for tests: 16 bytes more than come, so that the waits run out)
+      sm100::mbar_arrive_expect_tx(bar, DK * DV * 4 + (stall ? 16 : 0));
       for (int x = 0; x < DV / 32; ++x) sm100::tma_load_3d(sm + L::S + x * BOX, &map_s, bar, 32 * x, 0, (int)bh);
       bad[0] = 0u;
     }
@@ -275,10 +277,6 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
 
   // ---- read: D[c][i] = sum_r S[r][c] x_i[r]
   const bool here = sm100::mbar_drain(bar, 0, kWaitNs);
-  if (!here) {
-    if (lane == 0) atomicExch(status, (int)LA_ERR_TIMEOUT);
-    (void)sm100::mbar_drain(bar, 0, kWaitNs);      // nothing in flight when the CTA ends
-  }
   const int c0 = 16 * warp + 2 * g;
   float acc[2][4] = {}, acck[2][4] = {};           // (acck: delta rule)
   uint32_t vr[2][2];                               // delta: this lane's values of v
@@ -324,7 +322,13 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
       }
     }
   }
-  __syncthreads();                                 // W, 1 / den, the inverse triangle
+  // W, 1 / den, the inverse triangle; without its state the CTA ends here and
+  // stores nothing, after another wait for what may still be in flight
+  if (__syncthreads_or(!here)) {
+    (void)sm100::mbar_drain(bar, 0, kWaitNs);
+    if (tid == 0) atomicExch(status, (int)LA_ERR_TIMEOUT);
+    return;
+  }
 
   uint32_t a[4], al[4];                            // v or u as the A operand
   if constexpr (kDelta) {
@@ -424,7 +428,8 @@ cudaError_t launch(const TreeArgs& a) {
   const unsigned late1 = a.BH >= 4LL * resident ? (unsigned)resident : 0u, late0 = late1 / 2;
   kern<<<a.BH, L::NT + 32, L::BYTES, a.stream>>>(map_s, a.S, a.z, (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.k,
                                                  (const __nv_bfloat16*)a.v, a.parent, a.count, (__nv_bfloat16*)a.out,
-                                                 a.H, a.T, a.alpha, a.eps, status, late0, late1);
+                                                 a.H, a.T, a.alpha, a.eps, status, take_tree_timeout_test() ? 1 : 0,
+                                                 late0, late1);
   e = cudaGetLastError();
   if (e == cudaSuccess) note_launch();
   return e;

@@ -111,7 +111,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
                  const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
                  const __nv_bfloat16* __restrict__ v, const int* __restrict__ parent, const int* __restrict__ count,
                  __nv_bfloat16* __restrict__ out, int H, int ntok, const float* __restrict__ alpha, float eps,
-                 int* status) {
+                 int* status, int stall) {
   using Sh = Wide<DK, DV, TM, kDelta>;
   constexpr int NT = Sh::NT, NW = Sh::NW, SLAB = Sh::SLAB, SLABS = Sh::SLABS, BUF = Sh::BUF, QP = Sh::QP, VP = Sh::VP, WP = Sh::WP,
                 KS = DK / 16, NTM = TM / 8;
@@ -136,6 +136,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
   float* tri = reinterpret_cast<float*>(sm + L.tri);     // [block][16][16]: A on the diagonal
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bar);
   uint64_t* empty = full + 2;
+  volatile int* abort = reinterpret_cast<volatile int*>(bad + 2);        // a wait gave up
   const uint32_t base = sm100::smem_u32(sm);
   const __nv_bfloat16* qb = q + bh * (long long)ntok * DK;
   const __nv_bfloat16* kb = k + bh * (long long)ntok * DK;
@@ -146,7 +147,8 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
 
   auto load_slab = [&](int s) {                    // lane 0 of the extra warp
     uint64_t* bar = full + (s & 1);
-    sm100::mbar_arrive_expect_tx(bar, BUF);
+    // (stall, for tests: 16 bytes more than come, so that the waits run out)
+    sm100::mbar_arrive_expect_tx(bar, BUF + (stall && s == 0 ? 16 : 0));
     for (int x = 0; x < DV / 32; ++x)
       sm100::tma_load_3d(sm + L.ring + (s & 1) * BUF + x * (SLAB * 128), &map_s, bar, 32 * x, SLAB * s, (int)bh);
   };
@@ -162,9 +164,10 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
         prefetch_l2(S + bh * (long long)(DK * DV), DK * DV * 4);
       } else {
         load_slab(0);
-        if (SLABS > 1) load_slab(1);
+        load_slab(1);
       }
       bad[0] = bad[1] = 0u;
+      *abort = 0;
     }
     __syncwarp();
     tree_masks(parent + (long long)b * ntok, n, TP, mask, depth, reinterpret_cast<int*>(sm + L.up));
@@ -337,10 +340,11 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
       if (kDelta) acck[nt][e] = 0.f;
     }
   const int c0 = 16 * warp + 2 * g;                // this lane's columns: c0, c0 + 1
+  int lost = 0;                                    // a wait gave up: nothing is stored
   if (warp == NW) {
     if (L.overlay && lane == 0) {
       load_slab(0);
-      if (SLABS > 1) load_slab(1);
+      load_slab(1);
     }
     __syncwarp();
     if constexpr (kDelta)
@@ -350,13 +354,18 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
       }
     __syncwarp();
     if (lane == 0) {
-      for (int s = 2; s < SLABS; ++s) {
-        if (!sm100::mbar_drain(empty + (s & 1), ((s >> 1) - 1) & 1, kWaitNs)) atomicExch(status, (int)LA_ERR_TIMEOUT);
+      int s = 2;
+      for (; s < SLABS; ++s) {
+        if (!sm100::mbar_wait(empty + (s & 1), ((s >> 1) - 1) & 1, abort, kWaitNs)) {
+          lost = 1;
+          break;
+        }
         load_slab(s);
       }
-      // nothing in flight when the CTA ends, whatever became of the others
-      for (int s = SLABS > 1 ? SLABS - 2 : 0; s < SLABS; ++s)
-        if (!sm100::mbar_drain(full + (s & 1), (s >> 1) & 1, kWaitNs)) atomicExch(status, (int)LA_ERR_TIMEOUT);
+      // nothing in flight when the CTA ends, whatever became of the others: the
+      // last two slabs that were asked for (the ones before them have been read)
+      for (int x = s - 2; x < s; ++x)
+        if (!sm100::mbar_drain(full + (x & 1), (x >> 1) & 1, kWaitNs)) lost = 1;
     }
     __syncwarp();
     if (!kDelta)
@@ -375,7 +384,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
     const uint8_t* odd = box + (2 * t + 1) * 128 + ((piece ^ (2 * t + 1)) << 4);
 #pragma unroll
     for (int s = 0; s < SLABS; ++s) {
-      (void)sm100::mbar_drain(full + (s & 1), (s >> 1) & 1, kWaitNs);
+      if (!sm100::mbar_wait(full + (s & 1), (s >> 1) & 1, abort, kWaitNs)) lost = 1;
 #pragma unroll
       for (int kk = 0; kk < SLAB / 16; ++kk) {
         const int at = (s & 1) * BUF + 2048 * kk;
@@ -412,7 +421,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
           }
       }
       __syncwarp();
-      if (lane == 0 && s + 2 < SLABS) sm100::mbar_arrive(empty + (s & 1));
+      if (lane == 0 && !lost && s + 2 < SLABS) sm100::mbar_arrive(empty + (s & 1));
     }
   }
   if constexpr (kDelta) {
@@ -431,7 +440,10 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap map_s, const float* __restr
         }
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(lost)) {
+    if (tid == 0) atomicExch(status, (int)LA_ERR_TIMEOUT);
+    return;
+  }
 
   uint32_t uh[kDelta ? NTM / 2 : 1][4], ul[kDelta ? NTM / 2 : 1][4];     // u as the A operand, block by block
   if constexpr (kDelta) {
@@ -547,6 +559,7 @@ cudaError_t launch(const TreeArgs& a) {
   static_assert(!kDelta || (TM * (2 * (TM + 1) + DV) * 4 <= most.mask && 32 * (2 * 33 + DV) * 4 <= Sh(32).mask &&
                             (TM == 32 || 48 * (2 * 49 + DV) * 4 <= middle.mask)),
                 "room for delta_tree_by_paths");
+  static_assert(Sh::SLABS >= 2, "both buffers are filled first");
   static_assert(most.ring % 1024 == 0 && Sh::BUF % 1024 == 0, "the swizzle goes by address bits");
   const Sh L((a.T + 15) & ~15);
   auto kern = tree_wide_kernel<DK, DV, TM, kDelta>;
@@ -561,7 +574,7 @@ cudaError_t launch(const TreeArgs& a) {
   if (e != cudaSuccess) return e;
   kern<<<a.BH, Sh::NT + 32, L.total, a.stream>>>(map_s, a.S, a.z, (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.k,
                                                  (const __nv_bfloat16*)a.v, a.parent, a.count, (__nv_bfloat16*)a.out,
-                                                 a.H, a.T, a.alpha, a.eps, status);
+                                                 a.H, a.T, a.alpha, a.eps, status, take_tree_timeout_test() ? 1 : 0);
   e = cudaGetLastError();
   if (e == cudaSuccess) note_launch();
   return e;

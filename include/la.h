@@ -591,6 +591,15 @@ LA_API la_status la_device_status(int clear);
 LA_API void la_test_timeout_next_forward(void);
 
 /*
+ * The same for the next tensor-core la_decode_tree or la_decode_tree_delta
+ * (la_tree_path 1): its first copy of the state never counts as complete, the
+ * waits for it give up after their limit (2 s, and once more for what may be
+ * in flight), nothing is stored to `out`, and la_device_status reports
+ * LA_ERR_TIMEOUT. One-shot, process-wide; it faults nothing.
+ */
+LA_API void la_test_timeout_next_tree(void);
+
+/*
  * Forward pass for callers that cannot allocate device memory.
  *
  * The pages describe no counterpart to this entry point: it exists for
