@@ -17,8 +17,13 @@
 // probability e, so the sums need far more than fp32. fp64 would do, but its
 // pipe gives a warp's addition once in 64 cycles here (64 chains over 131072
 // tokens with the joins alone in fp64: 79 us): all sums are pairs of fp32
-// words with the rounding error of every addition kept (about 46 bits). p - q
-// is kept whole in the same way.
+// words, and p - q is kept whole in the same way. With u = 2^-24 a lane's sums
+// over 16 values are off by 140 u^2 of themselves at most (the words' rounding
+// errors are added up in fp32), a join of two pairs by 3 u^2; a lane joins 64
+// such sums before they meet the rest. In all 2^-38 of the row's sum for up to
+// 2^18 tokens, 2^-35 for 2^24, 2^-30 for 2^30 at worst; rows of random weights
+// come out within 2^-48. (One plain fp32 sum of all of a lane's rounding errors
+// had 2^-38 there with 4096 values a lane, 2^-25 with 32768.)
 //
 // One thread-block cluster per sequence: each CTA takes a contiguous part of
 // the vocabulary, each warp a contiguous part of that, so that the joined
@@ -195,7 +200,8 @@ struct Part {
   }
 };
 
-// This warp's sum of the weights of tokens [t0, t1). vec: every row starts on
+// This warp's sum of the weights of tokens [t0, t1), in groups of up to 16
+// values and 64 groups (the precision above). vec: every row starts on
 // a 16-byte boundary (t0 and t1 are multiples of a load then, or t1 = V is).
 // Rows that start anywhere are read a value at a time, US loads in flight: 16
 // for the tree (25.3 us for the trees below with 8, 24.0 with 16), 8 for the
@@ -210,6 +216,16 @@ __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
     float r;
     two_sum(hi, w.h, hi, r);
     lo += w.l + r;
+  };
+  Pair group = {0.f, 0.f}, sum = {0.f, 0.f};
+  int folds = 0;
+  auto fold = [&] {
+    group = group + normalised(hi, lo);
+    hi = lo = 0.f;
+    if ((++folds & 63) == 0) {
+      sum = sum + group;
+      group = {0.f, 0.f};
+    }
   };
   // (batches of loads under their own bounds: a loop's remainder would wait for
   // every load by itself)
@@ -229,7 +245,7 @@ __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
         }
       }
 #pragma unroll
-      for (int i = 0; i < U; ++i)
+      for (int i = 0; i < U; ++i) {
         if (tb + i * 32 * N < t1) {
           if (q != nullptr) {
 #pragma unroll
@@ -239,6 +255,8 @@ __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
             for (int e = 0; e < N; ++e) add(weight(x[i].get(e)));
           }
         }
+        if ((i + 1) * N % 16 == 0) fold();
+      }
     }
   } else {
     constexpr int U = US;
@@ -255,9 +273,10 @@ __device__ Pair span_total(const T* p, const T* q, int t0, int t1, bool vec) {
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) add(q != nullptr ? weight(x[i], y[i]) : weight(x[i]));
+      fold();
     }
   }
-  return warp_total(normalised(hi, lo));
+  return warp_total(sum + group);
 }
 
 // The sums of all warps' parts of a row, in every CTA (one cluster barrier).
@@ -362,7 +381,8 @@ __device__ int draw(const T* p, const T* q, int V, const Found& f, int rank, int
   }
   __syncthreads();
   if (warp == sh.piece) {
-    Pair before = sh.found_part.before;
+    const Pair before = sh.found_part.before;
+    Pair passed = {0.f, 0.f};                  // the piece's sum so far: joins of it are off by less than those of `before`
     const bool end = sh.found_part.end;
     int pick = -1;
     for (int t = t0; t < t1; t += 32) {
@@ -375,12 +395,12 @@ __device__ int draw(const T* p, const T* q, int V, const Found& f, int rank, int
       if (weighed == 0u) continue;
       pick = t + 31 - __clz(weighed);
       if (end) continue;
-      const unsigned hit = __ballot_sync(0xffffffffu, some && before + upto > f.want);
+      const unsigned hit = __ballot_sync(0xffffffffu, some && before + (passed + upto) > f.want);
       if (hit != 0u) {
         pick = t + __ffs(hit) - 1;
         break;
       }
-      before = before + from_lane(upto, 31);
+      passed = passed + from_lane(upto, 31);
     }
     if (lane == 0) sh.found = pick;
   }

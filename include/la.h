@@ -407,7 +407,8 @@ LA_API la_status la_decode_tree_delta(const float* S, const void* q, const void*
  * times all of them (the last positive weight where rounding leaves none).
  * Weights need not be normalised; those that are not above zero (NaN too) are
  * zero. A row with no positive weight, or an infinite one, gives next = -1.
- * Sums carry about 48 bits. T <= LA_TREE_MAX; T = 0 just draws (draft and
+ * Sums are off by less than 2^-38 of the row's sum for V up to 2^18, 2^-35 up
+ * to 2^24 and 2^-30 beyond, whatever the weights. T <= LA_TREE_MAX; T = 0 just draws (draft and
  * tokens may be NULL); 1 <= V <= 2^30. target and draft 16-byte aligned.
  */
 LA_API la_status la_verify_chain(const void* target, const void* draft, const int* tokens, const int* count,
