@@ -49,9 +49,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// a and b as bf16 pairs: high parts and what they leave
+// a and b as bf16 pairs: high parts and what they leave. A high part stops at
+// bf16's largest number, 2^128 - 2^120: fp32 goes on up to 2^128 - 2^104, and an
+// infinite high part would leave -inf (or, for an infinite value, NaN). So the
+// low part has what is beyond, infinities too, and a product with them is
+// infinite and not NaN.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack2(a, b);
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
   lo = pack2(a - low_half(hi), b - high_half(hi));
 }
 

@@ -246,9 +246,10 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
         for (int p = 0; p < KW; ++p) w += part[p * TP * PP + i * PP + j];
         if (!kDelta && alpha != nullptr) w *= pw[depth[i] - depth[j]];
       }
-      const __nv_bfloat16 hi = __float2bfloat16_rn(w);
-      *reinterpret_cast<__nv_bfloat16*>(sm + L::WH + i * WPB + 2 * j) = hi;
-      *reinterpret_cast<__nv_bfloat16*>(sm + L::WL + i * WPB + 2 * j) = __float2bfloat16_rn(w - __bfloat162float(hi));
+      uint32_t hi, lo;
+      split2(w, 0.f, hi, lo);
+      *reinterpret_cast<uint16_t*>(sm + L::WH + i * WPB + 2 * j) = (uint16_t)hi;
+      *reinterpret_cast<uint16_t*>(sm + L::WL + i * WPB + 2 * j) = (uint16_t)lo;
       if constexpr (kDelta) {
         float a = 0.f;
         if (on && i != j) {
