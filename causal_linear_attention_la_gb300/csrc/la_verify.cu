@@ -126,9 +126,12 @@ __device__ __forceinline__ Pair warp_total(Pair x) {
 }
 
 // u * q < p for fp32 numbers, exactly: the product's rounding error decides a
-// tie. Tiny numbers are scaled up first, so that the error does not underflow.
+// tie. Where p is tiny, both sides are scaled up first, so that neither a tie's
+// product (it is near p) nor its error, 2^-48 of it at least, underflows. With q
+// at 2^60 or more and p below 2^-60 there is no tie: u would be below 2^-120 and
+// the product still 2^-89, which leaves its error room.
 __device__ __forceinline__ bool stands(float u, float q, float p) {
-  if (fabsf(q) < 0x1p-60f && fabsf(p) < 0x1p-60f) {
+  if (fabsf(p) < 0x1p-60f && fabsf(q) < 0x1p60f) {
     q *= 0x1p60f;
     p *= 0x1p60f;
   }

@@ -1,6 +1,7 @@
-"""Draws from rows of many dense weights, next to a border.
+"""Draws from rows of many dense weights, next to a border, and acceptance tests
+next to a tie.
 
-Every weight here is a whole number of units, so that the sums are known exactly
+Every weight there is a whole number of units, so that the sums are known exactly
 in 64-bit integers and one weight can be set such that the draw lies a chosen
 distance from the border between two tokens. The stated bound of the kernel's
 sums (2^-38 of the row's sum up to 2^18 tokens, 2^-35 up to 2^24) is the distance.
@@ -97,3 +98,33 @@ def test_draw_from_the_rest_next_to_a_border(V, B, bits):
     tokens = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")       # no token of the vocabulary: it falls
     accepted, nxt = la.verify_chain(p, draft, tokens, torch.from_numpy(u).cuda())
     assert not accepted.any() and np.array_equal(nxt.cpu().numpy(), want)
+
+
+def test_acceptance_next_to_a_tie():
+    """u q < p exactly (64 bits hold the product of two fp32 numbers), for numbers
+    of any size: p is the rounded product, one step below or one above."""
+    import torch
+    rng = np.random.default_rng(2)
+    u, q, p = [], [], []
+    for eu, eq in [(0, 0), (-24, -10), (-30, -59), (-30, -62), (-60, -30), (-100, -30), (-120, -20), (-140, 0), (-148, 40), (-60, -85),
+                   (-10, -130), (-90, 59), (-125, 70)]:
+        for _ in range(40):
+            a = np.float32(2.0 ** (eu - 1) * (1 + rng.random()))
+            b = np.float32(2.0 ** eq * (1 + rng.random()))
+            x = np.float32(np.float64(a) * np.float64(b))
+            u += [a] * 3
+            q += [b] * 3
+            p += [x, np.nextafter(x, np.float32(0)), np.nextafter(x, np.float32(np.inf))]
+    u += [np.float32(2.0 ** -100)]                       # 2^-130 (1 - 2^-24), a subnormal 2^-130 once rounded
+    q += [np.float32(2.0 ** -30 * (1 - 2.0 ** -24))]
+    p += [np.float32(2.0 ** -130)]
+    u, q, p = (np.array(x, np.float32) for x in (u, q, p))
+    B, V = len(u), 8
+    target, draft = np.zeros((B, 2, V), np.float32), np.zeros((B, 1, V), np.float32)
+    target[:, 0, 3], target[:, 1, 5], draft[:, 0, 3] = p, 1.0, q
+    uniform = np.stack([u, np.full(B, 0.5, np.float32)], 1)
+    tokens = torch.full((B, 1), 3, dtype=torch.int32, device="cuda")
+    accepted, _ = la.verify_chain(*(torch.from_numpy(x).cuda() for x in (target, draft)), tokens, torch.from_numpy(uniform).cuda())
+    want = u.astype(np.float64) * q.astype(np.float64) < p.astype(np.float64)
+    assert want[-1] and 0.2 < want.mean() < 0.8
+    assert np.array_equal(accepted.cpu().numpy(), want.astype(np.int32))
