@@ -71,6 +71,65 @@ def decode_tree_delta(S, q, k, v, parent, count=None):
     return out, scale
 
 
+def decode_tree_delta_bound(S, q, k, v, parent, count=None, parts=False):
+    """How far a delta-rule tree decode may be off before its result is rounded,
+    [B,H,T,dv]. Where ``scale`` of decode_tree_delta adds up magnitudes along a
+    path and grows with every token, this takes the increments themselves:
+
+    With A_jl = k_j.k_l and W_ij = q_i.k_j along the paths, M = (I + A)^-1 and
+    R = v - S^T k, the increments are U = M R and out = S^T q + W U. If U_hat
+    solves (I + A) U_hat = R + rho, it is off by at most |M| |rho|. Let u = 2^-24.
+
+    parts=False: fp32 throughout. A sum of m products is off by (m + 4) u of its
+    terms' magnitudes, so that rho has (dk + 4) u |S|^T |k|, 2 u (|v| + |S|^T |k|)
+    for the difference, (dk + 4) u |k_j|.|k_l| |U_l| for the key products and
+    (T + 4) u |A| |U| for the substitution.
+
+    parts=True: fp32 operands as two bf16 parts, x = hi + lo up to 2^-17 of x, and
+    products of two of them without lo lo: up to 2^-15 of the term. A sum of m
+    terms on the tensor cores is off by 4 m u: three products a term and sums
+    that truncate. The solve goes block by block of 16 nodes, U_b = X_b R'_b with
+    X_b the inverse of the block's own triangle L_b (the same block of M) and R'_b
+    = L_b U_b what the earlier blocks leave, so that an error of the product with
+    X_b counts as L_b times it in rho; X_b itself, by substitution, is off by
+    32 u |X| |L| |X| and by its triangle's errors.
+
+    Errors of second order are allowed for by 5 %."""
+    S, q, k, v = _as64(S, q, k, v)
+    B, H, T, dk = q.shape
+    bound = np.full(v.shape, np.nan)
+    u = 2.0 ** -24
+    split, pair = (2.0 ** -17, 2.0 ** -15) if parts else (0.0, 0.0)
+    acc = (lambda m: 4 * m * u) if parts else (lambda m: (m + 4) * u)
+    for b in range(B):
+        n = T if count is None else min(max(int(count[b]), 0), T)
+        on = np.zeros((n, n), bool)
+        for i in range(n):
+            on[i, path_of(parent[b], i)] = True
+        below = on & ~np.eye(n, dtype=bool)
+        block = np.arange(n) // 16
+        same = block[:, None] == block[None]
+        for h in range(H):
+            S_, q_, k_, v_ = S[b, h], q[b, h, :n], k[b, h, :n], v[b, h, :n]
+            A, W = np.where(below, k_ @ k_.T, 0.0), np.where(on, q_ @ k_.T, 0.0)
+            kk, qk = np.where(below, np.abs(k_) @ np.abs(k_).T, 0.0), np.where(on, np.abs(q_) @ np.abs(k_).T, 0.0)
+            M = np.linalg.inv(np.eye(n) + A)
+            U = M @ (v_ - k_ @ S_)
+            aU, read = np.abs(U), np.abs(k_) @ np.abs(S_)
+            rho = (split + acc(dk)) * read + 2 * u * (np.abs(v_) + read)
+            if parts:
+                L, X = np.eye(n) + np.where(same, A, 0.0), np.abs(np.where(same, M, 0.0))
+                rho += (pair + acc(64)) * np.where(same, 0.0, np.abs(A)) @ aU + acc(dk) * np.where(same, 0.0, kk) @ aU
+                XR = X @ np.abs(L @ U)
+                own = (pair + acc(48)) * XR + X @ (acc(dk) * np.where(same, kk, 0.0) + 32 * u * np.abs(L)) @ XR
+                rho += np.abs(L) @ own
+            else:
+                rho += acc(T) * np.abs(A) @ aU + acc(dk) * kk @ aU
+            off = (split + acc(dk)) * (np.abs(q_) @ np.abs(S_)) + acc(dk) * qk @ aU + (pair + acc(64)) * np.abs(W) @ aU
+            bound[b, h, :n] = 1.05 * (off + np.abs(W) @ (np.abs(M) @ rho))
+    return bound
+
+
 def advance(S, z, k, v, path=None, accepted=None, alpha=None):
     """State after each sequence's accepted rows; returns (S, z, scale of S)."""
     S, z, k, v = (x.copy() for x in _as64(S, z, k, v))
@@ -99,6 +158,27 @@ def advance_delta(S, k, v, path=None, accepted=None):
             S[b] = S[b] + kj[:, :, None] * u[:, None, :]
             A[b] = A[b] + np.abs(kj)[:, :, None] * au[:, None, :]
     return S, A
+
+
+def advance_delta_bound(S, k, v, path=None, accepted=None):
+    """How far an fp32 state advance by the delta rule may be off, like S. A step
+    takes an error E of the state to (I - k k^T) E, whose columns grow by at most
+    max(1, | |k|^2 - 1 |) in the 2-norm, and adds its own: (dk + 4) u of |S|^T |k| in
+    u = S^T k and 2 u of |v| + |S|^T |k| in v - u, times |k|, and u of the new state
+    (u = 2^-24). Every value of a column is off by at most the column's norm; 5 %
+    for errors of second order."""
+    S, k, v = (x.copy() for x in _as64(S, k, v))
+    B, _, T, dk = k.shape
+    u, err = 2.0 ** -24, np.zeros((S.shape[0], S.shape[1], S.shape[3]))
+    for b in range(B):
+        for j in _rows(path, accepted, b, T):
+            kj, vj = k[b, :, j], v[b, :, j]
+            size = np.einsum("hkv,hk->hv", np.abs(S[b]), np.abs(kj))
+            off = (dk + 4) * u * size + 2 * u * (np.abs(vj) + size)
+            S[b] = S[b] + kj[:, :, None] * (vj - np.einsum("hkv,hk->hv", S[b], kj))[:, None, :]
+            norm = np.linalg.norm(kj, axis=-1)[:, None]
+            err[b] = err[b] * np.maximum(1.0, np.abs(norm ** 2 - 1)) + norm * off + u * np.linalg.norm(S[b], axis=1)
+    return np.broadcast_to(1.05 * err[:, :, None, :], S.shape)
 
 
 def _rows(path, accepted, b, T):
