@@ -103,6 +103,9 @@ la_status pack_call(const char* who, const PackArgs& a, bool pack) {
   la_status st = check_states(who, a.B, a.H, 0, a.dk, a.dv, LA_F32, &empty);
   if (st != LA_OK) return st;
   if (a.slots < 0) return fail(LA_ERR_INVALID_ARG, "%s: negative number of slots", who);
+  // every CTA looks through the later sequences' slots: B^2 reads in all, which
+  // take minutes from 2^24 sequences on
+  if (pack && a.B > (1 << 20)) return fail(LA_ERR_UNSUPPORTED, "%s: B=%d sequences, at most %d", who, a.B, 1 << 20);
   if ((a.z == nullptr) != (a.z_pool == nullptr))
     return fail(LA_ERR_INVALID_ARG, "%s: z and z_pool must be both given or both NULL", who);
   // one sequence's states are indexed with 32 bits, one CTA takes 4096 values

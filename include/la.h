@@ -480,7 +480,8 @@ LA_API la_status la_state_advance_delta(const float* S, const void* k, const voi
  *        Several sequences may be unpacked from one slot; where several are
  *        packed into one, the last of them is what it holds.
  * The way back is exact, and packing an unpacked state again changes no value.
- * S, z, codes, z_pool 16-byte aligned, not overlapping. H*dk*dv <= 2^30.
+ * S, z, codes, z_pool 16-byte aligned, not overlapping. H*dk*dv <= 2^30; la_state_pack
+ * takes at most 2^20 sequences a call (each slot is looked for among the later ones).
  */
 LA_API la_status la_state_pack(const float* S, const float* z, unsigned char* codes, unsigned char* scales,
                                float* z_pool, const int* slot, int B, int H, int dk, int dv, int slots,

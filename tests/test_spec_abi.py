@@ -159,3 +159,11 @@ def test_python_shape_checks():
         la._need_like(-1, ("a", t.t(), torch.float32, (3, 2)))
     with pytest.raises(ValueError, match="on cuda:0"):
         la._need_like(0, ("a", t, torch.float32, (2, 3)))
+
+
+def test_pack_refuses_more_sequences_than_it_can_look_through(lib):
+    """Each CTA reads the slots of all later sequences: B^2 / 2 reads."""
+    c = dict(S=1024, z=None, codes=1024, scales=1024, z_pool=None, slot=1024, H=1, dk=16, dv=16, slots=0, stream=None)
+    assert la.la_state_pack(B=1 << 20, **c) == OK                 # (no slots: nothing is launched)
+    assert la.la_state_pack(B=(1 << 20) + 1, **c) == UNSUPPORTED and b"at most 1048576" in lib.la_last_error()
+    assert la.la_state_unpack(B=(1 << 20) + 1, **c) == OK
