@@ -411,7 +411,8 @@ __device__ int draw(const T* p, const T* q, int V, const Found& f, int rank, int
   return sh.found;
 }
 
-// A total that can be drawn from (an infinite weight makes it no number).
+// A total that can be drawn from (an infinite weight, or more than fp32 holds,
+// makes it infinite or no number).
 __device__ __forceinline__ bool drawable(Pair total) { return total.h > 0.f && total.h <= 3.4e38f; }
 
 template <typename T>

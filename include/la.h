@@ -406,9 +406,11 @@ LA_API la_status la_decode_tree_delta(const float* S, const void* q, const void*
  * A draw with u takes the smallest t whose weights 0 .. t sum to more than u
  * times all of them (the last positive weight where rounding leaves none).
  * Weights need not be normalised; those that are not above zero (NaN too) are
- * zero. A row with no positive weight, or an infinite one, gives next = -1.
- * Sums are off by less than 2^-38 of the row's sum for V up to 2^18, 2^-35 up
- * to 2^24 and 2^-30 beyond, whatever the weights. T <= LA_TREE_MAX; T = 0 just draws (draft and
+ * zero. A row with no positive weight, an infinite one, or weights that sum to
+ * more than 3.4e38 gives next = -1. Sums are off by less than 2^-38 of the row's
+ * sum for V up to 2^18, 2^-35 up to 2^24 and 2^-30 beyond, whatever the weights
+ * (below a sum of 2^-110, fp32's smallest numbers end that).
+ * T <= LA_TREE_MAX; T = 0 just draws (draft and
  * tokens may be NULL); 1 <= V <= 2^30. target and draft 16-byte aligned.
  */
 LA_API la_status la_verify_chain(const void* target, const void* draft, const int* tokens, const int* count,

@@ -128,3 +128,27 @@ def test_acceptance_next_to_a_tie():
     want = u.astype(np.float64) * q.astype(np.float64) < p.astype(np.float64)
     assert want[-1] and 0.2 < want.mean() < 0.8
     assert np.array_equal(accepted.cpu().numpy(), want.astype(np.int32))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 50001])
+def test_rows_that_sum_past_fp32(V, dtype):
+    """Finite weights whose sum is beyond 3.4e38 give no token, wherever they lie;
+    just below it they are drawn from, and so are sums of 2^-110."""
+    import torch
+    from helpers import to_dev
+    w = np.zeros((6, 2, V), np.float32)
+    w[0, :, [0, V - 1]] = 2.0 ** 127                     # 2^128
+    w[1, :, ::7] = 2.0 ** 126
+    w[2, :, [0, V - 1]] = 2.0 ** 126                     # 2^127: drawn from
+    w[3, :, [1, V - 2]] = 2.0 ** -111
+    w[4, :, :30] = 2.0 ** 124                            # 30 of 16
+    w[5, :, :15] = 2.0 ** 124                            # 15 of 16: drawn from
+    u = np.full((6, 2), 0.75, np.float32)
+    want = [-1, -1, V - 1, V - 2, -1, 11]
+    p = to_dev(w, dtype)
+    none = torch.full((6, 1), -1, dtype=torch.int32, device="cuda")
+    accepted, nxt = la.verify_chain(p, torch.zeros_like(p[:, :1]), none, torch.from_numpy(u).cuda())
+    assert not accepted.any() and nxt.tolist() == want
+    path, accepted, nxt = la.verify_tree(p, none, none, torch.from_numpy(u).cuda())
+    assert not accepted.any() and nxt.tolist() == want and torch.all(path == -1)
