@@ -486,11 +486,14 @@ tree_verify_kernel(const T* __restrict__ target, const int* __restrict__ tokens,
     token = -1;
     int child = -1;
     if (drawable(f.total)) {
-      const int t = f.part / VW == rank ? draw<T>(p, nullptr, V, f, rank, nc, sh) : -1;
-      if (t >= 0 && threadIdx.x < 32) {
-        // the first child that holds the token
+      const bool mine = f.part / VW == rank;
+      const int t = mine ? draw<T>(p, nullptr, V, f, rank, nc, sh) : -1;
+      if (mine && threadIdx.x < 32) {
+        // the first child that holds the token (told in any case: a row that
+        // changed since it was summed, by a caller's mistake, may give none, and
+        // the others would go by what lies in their memory)
         int hit = -1;
-        for (int i0 = 0; i0 < all && hit < 0; i0 += 32) {
+        for (int i0 = 0; t >= 0 && i0 < all && hit < 0; i0 += 32) {
           const int i = i0 + lane;
           const unsigned m = __ballot_sync(0xffffffffu, i < all && i > at && sh.par[i] == at && sh.tok[i] == t);
           if (m != 0u) hit = i0 + __ffs(m) - 1;
