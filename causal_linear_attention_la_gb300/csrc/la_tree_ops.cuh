@@ -11,11 +11,15 @@
 // take 8 cycles an instruction here and hide under the loads.)
 //
 // Precision: fp32 operands go in as bf16 high and low parts, x = hi + lo + e
-// with |e| <= 2^-18 |x| (two roundings to nearest of 2^-9 each), and the
-// products hi hi + lo hi + hi lo leave out lo lo, 2^-18 of the term at most:
-// below 2^-16 of the sum of the terms' magnitudes in all, far under the 2^-9 of
-// the bf16 result. Rows that are bf16 as they are (the delta rule's q and k,
-// and v) have no low part. Sums are fp32.
+// with |lo| <= 2^-8 |x| and |e| <= 2^-17 |x| (bf16 rounds by up to 2^-8, and what
+// it leaves is below half a step of hi). The products hi hi + lo hi + hi lo leave
+// out lo lo, up to 2^-16 of the term: with both operands' e a product is off by
+// 2^-15 of itself at most. A pair weight is such a product (2^-15), split again
+// before it meets v (2^-17), and the denominator sums the weights (2^-15): an
+// output is off by 2^-13.8 of the sum of its terms' magnitudes at worst, 2^-17.5
+// on random rows, besides its own rounding of 2^-8. A fourth product for lo lo
+// would take a third more mma and leave 2^-14.6. Rows that are bf16 as they are
+// (the delta rule's q and k, and v) have no low part. Sums are fp32.
 //
 // Weights of nodes off a path are zeros in the products, which would turn an
 // infinite or NaN value into NaN for everybody: such values are left out of
@@ -59,7 +63,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack2(a - low_half(hi), b - high_half(hi));
 }
 
-// phi from one exponential: 2^-21 of the value, well inside the 2^-18 of its
+// phi from one exponential: 2^-21 of the value, well inside the 2^-17 of its
 // two bf16 parts (|x| log2(e) is rounded to 2^-24 of itself, and beyond |x| = 8
 // phi is below 2^-11 of the 1 that a zero gives)
 __device__ __forceinline__ float phi_fast(float x) {

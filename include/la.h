@@ -362,7 +362,8 @@ LA_API la_status la_state_copy(float* dst_S, float* dst_z, const float* src_S,
  * A node off a path never reaches its outputs, whatever its rows hold
  * (infinities and NaN included). fp32 arithmetic; where la_tree_path is 1 the
  * products run on the tensor cores, fp32 operands as bf16 high and low parts
- * (below 2^-16 of the sum of the terms' magnitudes), summed in fp32.
+ * (a term is off by up to 2^-15 of itself, an output by less than 2^-13 of the
+ * sum of its terms' magnitudes, both far less on usual rows), summed in fp32.
  */
 LA_API la_status la_decode_tree(const float* S, const float* z, const void* q, const void* k, const void* v,
                                 const int* parent, const int* count, void* out, int B, int H, int T, int dk,
