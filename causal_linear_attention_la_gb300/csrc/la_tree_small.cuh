@@ -82,8 +82,8 @@ tree_small_kernel(const __grid_constant__ CUtensorMap map_s, const float* __rest
   extern __shared__ __align__(1024) uint8_t sm[];
   const long long bh = blockIdx.x;
   const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // an SM's two CTAs start at once and then keep step, both at their loads and
-  // both at their products: the second one starts a third of a CTA later
+  // an SM's first CTAs start at once and then keep step, all at their loads and
+  // all at their products: half of them start 1.5 us later
   if (blockIdx.x >= late0 && blockIdx.x < late1) __nanosleep(1500);
   const int n = clamp_count(count, b, ntok);
   if (n == 0) return;
@@ -424,8 +424,13 @@ cudaError_t launch(const TreeArgs& a) {
   CUtensorMap map_s;
   e = state_map<DK, DV>(&map_s, a.S, a.BH, DK);
   if (e != cudaSuccess) return e;
-  // (worth its wait with several CTAs to come for each place: 16 nodes on 2048
-  // states 31.6 -> 30 us; none for a call that is over after a few)
+  // Worth its wait with several CTAs to come for each place, none for a call that
+  // is over after a few. Without and with it, 16 nodes on 2048, 4096 and 8192
+  // states, us: d = 128 32.4 31.2, 58.3 56.9, 109.5 108.1 (4 nodes on 2048 29.1
+  // 27.9); dk = 128, dv = 64 22.2 21.8, 39.7 39.1, 73.7 73.3; dk = 64, dv = 128
+  // 21.3 21.0, 37.9 37.7, 71.0 70.7; d = 64, four CTAs an SM, 12.8 12.8, 22.6
+  // 22.3, 40.7 40.5 (4 nodes 10.8 10.8, 19.6 19.7, 35.4 35.5). By the delta rule 1
+  // to 5 % less time, level at d = 64.
   const unsigned late1 = a.BH >= 4LL * resident ? (unsigned)resident : 0u, late0 = late1 / 2;
   kern<<<a.BH, L::NT + 32, L::BYTES, a.stream>>>(map_s, a.S, a.z, (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.k,
                                                  (const __nv_bfloat16*)a.v, a.parent, a.count, (__nv_bfloat16*)a.out,
