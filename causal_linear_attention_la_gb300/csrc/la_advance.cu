@@ -15,7 +15,8 @@
 // again, which leaves L2 to the writes: 2048 states by up to six tokens 44 us,
 // 0.91 of the floor (256 threads 52, 512 64; without the hints 46). The delta
 // rule joins its reads in shared memory once a token: four row groups of 128
-// threads instead of eight, 2048 states 70 -> 57 us. A sequence that accepted
+// threads instead of eight, 2048 states 70 -> 57 us; by up to six tokens 49 us,
+// 0.82 of the floor. A sequence that accepted
 // nothing is not touched in place and copied otherwise.
 #include "la_spec.cuh"
 

@@ -19,7 +19,7 @@
 // Up to 32 nodes three CTAs share an SM and slabs have 16 rows. Up to 48 nodes
 // the slabs have buffers of their own and start with the CTA; above, two CTAs
 // per SM leave no room and the buffers are where phi(k) was, from the pairs on.
-// 1536 decay-gated d = 128 states of up to 64 nodes: 59 us, the tensor pipe at
+// 1536 decay-gated d = 128 states of up to 64 nodes: 60 us, the tensor pipe at
 // 0.29, the issue slots at 0.41 - chains of dependent steps. What did not help:
 // the state straight from global memory into the lanes' registers (fragments
 // of 64 bytes, twice the wavefronts: 79 us), two warps per 16 columns (half as

@@ -380,7 +380,8 @@ LA_API int la_tree_path(int dk, int dv, la_dtype dtype);
  * increments along the paths solve one unit lower-triangular system,
  *   u_j = v_j - S^T k_j - sum_{l in anc(j), l != j} (k_j.k_l) u_l,
  *   out_i = S^T q_i + sum_{j in anc(i)} (q_i.k_j) u_j.
- * Arguments as la_decode_tree without z, alpha and eps.
+ * Arguments as la_decode_tree without z, alpha and eps; an error of an increment
+ * reaches the nodes below it as the increment itself does.
  */
 LA_API la_status la_decode_tree_delta(const float* S, const void* q, const void* k, const void* v,
                                       const int* parent, const int* count, void* out, int B, int H, int T,
