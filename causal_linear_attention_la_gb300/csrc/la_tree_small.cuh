@@ -429,8 +429,8 @@ cudaError_t launch(const TreeArgs& a) {
   // states, us: d = 128 32.4 31.2, 58.3 56.9, 109.5 108.1 (4 nodes on 2048 29.1
   // 27.9); dk = 128, dv = 64 22.2 21.8, 39.7 39.1, 73.7 73.3; dk = 64, dv = 128
   // 21.3 21.0, 37.9 37.7, 71.0 70.7; d = 64, four CTAs an SM, 12.8 12.8, 22.6
-  // 22.3, 40.7 40.5 (4 nodes 10.8 10.8, 19.6 19.7, 35.4 35.5). By the delta rule 1
-  // to 5 % less time, level at d = 64.
+  // 22.3, 40.7 40.5 (4 nodes 10.8 10.8, 19.6 19.7, 35.4 35.5). By the delta rule
+  // up to 5 % less time, level at d = 64.
   const unsigned late1 = a.BH >= 4LL * resident ? (unsigned)resident : 0u, late0 = late1 / 2;
   kern<<<a.BH, L::NT + 32, L::BYTES, a.stream>>>(map_s, a.S, a.z, (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.k,
                                                  (const __nv_bfloat16*)a.v, a.parent, a.count, (__nv_bfloat16*)a.out,

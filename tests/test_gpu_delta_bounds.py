@@ -74,6 +74,37 @@ def test_ragged_trees(count, dtype):
         check_tree(64, 128, 128, dtype, dtype == "bf16", correlated, count)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [14, 24, 47, 60])
+def test_nodes_beside_one_that_is_not_finite(T, d, dtype):
+    """Nodes whose paths are clean, held to the bound of the tree that is left
+    when the others are taken out."""
+    import torch
+    S, q, k, v, parent = inputs(T, d, d, T + d, correlated=2.0)
+    S, q, k, v = (x[2:] for x in (S, q, k, v))
+    parent, bad = parent[2], [2, 9]
+    clean = [i for i in range(T) if not set(spec.path_of(parent, i)) & set(bad)]
+    left = np.array([[clean.index(parent[i]) if parent[i] >= 0 else -1 for i in clean]])
+    rest = [x[:, :, clean] for x in (q, k, v)]
+    want, _ = spec.decode_tree_delta(S, *rest, left)
+    # (fp32 on the CUDA cores; on the tensor cores such a tree is done again in fp32)
+    bound = HALF[dtype] * np.abs(want) + spec.decode_tree_delta_bound(S, *rest, left)
+    for rows in (k, v):
+        for x in (np.nan, np.inf, -3e38):
+            was = rows[:, :, bad].copy()
+            rows[:, :, bad, 1::5] = x
+            out = la.decode_tree_delta(torch.from_numpy(S).cuda(), *[to_dev(y.astype(np.float32), dtype) for y in (q, k, v)],
+                                       i32(parent[None]))
+            rows[:, :, bad] = was
+            got = to_host(out)[:, :, clean]
+            if x != -3e38 or dtype == "f32":
+                assert np.all(np.abs(got - want) <= bound)
+            else:                                # finite until a product overflows: may stay on the tensor cores
+                parts = spec.decode_tree_delta_bound(S, *rest, left, parts=True)
+                assert np.all(np.abs(got - want) <= HALF[dtype] * np.abs(want) + parts)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 32), (16, 16), (32, 128)])
 @pytest.mark.parametrize("T", [1, 5, 8, 9, 33, 100])
