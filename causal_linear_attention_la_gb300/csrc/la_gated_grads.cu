@@ -12,8 +12,9 @@
 // is the sum from each token to the end. A pair (t, j) adds what it takes away in that
 // sum, once from row t and once from column j: both come from the same bf16 values of N and W, so that
 // it leaves nothing. (Rounded apart, the pairs' differences were 9e-3 of dg.) Where
-// |beta_j| < 2^-100 column j has 2^-100 in its place in N^T and W^T, whose row j
-// then counts beta_j 2^100 times.
+// |beta_j| < 2^-30 column j has 2^-30 in its place in N^T and W^T, whose row j
+// then counts beta_j 2^30 times (a power of two near the others' sizes: with 2^-100 gradients
+// of 1e-9 fell below bf16's normal numbers).
 // Products (M = 128, A and B in shared memory with the 128-byte swizzle, fp32 in
 // tensor memory; a lane is a token's row: lanes 0-63 of dK, 64-127 of dQ):
 //   1. [dR; dO] E^T                 [128 x 64]
@@ -39,7 +40,7 @@ using namespace sm100;
 
 constexpr int NT = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;       // bound of every wait for the tensor cores
-constexpr float kTiny = 7.888609052210118e-31f, kHuge = 1.2676506002282294e30f;   // 2^-100, 2^100
+constexpr float kTiny = 9.313225746154785e-10f, kHuge = 1073741824.f;   // 2^-30, 2^30
 
 // 32 lanes x 16 consecutive 32-bit columns of tensor memory.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
