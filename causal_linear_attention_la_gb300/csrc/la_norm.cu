@@ -12,7 +12,10 @@
 // Angles: freq / 2 pi as a 64-bit fraction F of a turn (an integer product with the
 // first 128 bits of 1 / 2 pi), the angle is the low 64 bits of position * F: exact
 // for every position up to the rounding of F, 2^-64 of a turn. (In fp64, F and its
-// conversions took 2600 cycles a warp: that pipe takes an instruction every 64.)
+// conversions took 2600 cycles a warp: that pipe takes an instruction every 64.) Of the
+// angle the top 32 bits go on. For bf16 rows their sine and cosine are the special
+// function unit's, off by 2^-21, a 2^12th of a bf16 step of 1; for fp32 rows sincospif of what is
+// left of whole quarters of a turn: off by 2^-25 and two steps of the value.
 #include "la_gated.cuh"
 
 namespace la {
@@ -86,7 +89,7 @@ __device__ __forceinline__ unsigned long long turn_fraction(float freq) {
 
 // Cosines and signed sines at a token: z_i = y_i c_i + y_partner s_i (1 and 0
 // where components are not turned). turns: F of every pair, in shared memory.
-template <int V, bool kInter>
+template <int V, bool kInter, bool kFine>
 __device__ __forceinline__ void angles(const NormKernelArgs& p, long long token, int n, int c0,
                                        const unsigned long long* turns, float (&cs)[V], float (&sn)[V]) {
   if (c0 >= p.rot) {
@@ -103,11 +106,22 @@ __device__ __forceinline__ void angles(const NormKernelArgs& p, long long token,
   const unsigned long long* f = turns + (kInter ? c0 / 2 : second ? c0 - half : c0);
 #pragma unroll
   for (int i = 0; i < (kInter ? V / 2 : V); ++i) {
-    // the top 32 of 64 bits: in [-1/2, 1/2) turns, off by 2^-32 of one; the
-    // sine and cosine of an angle in [-pi, pi] off by 2^-21
-    const int a = (int)(((unsigned long long)pos * f[i]) >> 32);
+    // the top 32 of 64 bits: in [-1/2, 1/2) turns, off by 2^-32 of one
+    const uint32_t a = (uint32_t)(((unsigned long long)pos * f[i]) >> 32);
     float s, c;
-    __sincosf((float)a * 1.4629180792671596e-9f, &s, &c);     // a pi 2^-31
+    if constexpr (kFine) {
+      const uint32_t quarter = (a + 0x20000000u) >> 30;
+      float s0, c0;
+      sincospif((float)(int)(a - (quarter << 30)) * 4.656612873077393e-10f, &s0, &c0);     // 2^-31
+      s = quarter & 1 ? c0 : s0;
+      c = quarter & 1 ? -s0 : c0;
+      if (quarter & 2) {
+        s = -s;
+        c = -c;
+      }
+    } else {
+      __sincosf((float)(int)a * 1.4629180792671596e-9f, &s, &c);     // a pi 2^-31
+    }
     if (kInter) {
       cs[2 * i] = cs[2 * i + 1] = c;
       sn[2 * i] = -s;
@@ -150,7 +164,7 @@ norm_rotate_kernel(const NormKernelArgs p) {
   const long long tk = live ? token : 0;
   const int b = (int)(tk / p.N), n = (int)(tk % p.N);
   float cs[V], sn[V];
-  if (kRot) angles<V, kInter>(p, tk, n, c0, turns, cs, sn);
+  if (kRot) angles<V, kInter, sizeof(T) == 4>(p, tk, n, c0, turns, cs, sn);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int Hi = i ? p.H1 : p.H0, off = i ? p.H0 : 0;
@@ -233,7 +247,7 @@ norm_rotate_backward_kernel(const NormKernelArgs p) {
     const long long tk = live ? token : 0;
     const int b = (int)(tk / p.N), n = (int)(tk % p.N);
     float cs[V], sn[V];
-    if (kRot) angles<V, kInter>(p, tk, n, c0, turns, cs, sn);
+    if (kRot) angles<V, kInter, sizeof(T) == 4>(p, tk, n, c0, turns, cs, sn);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int Hi = i ? p.H1 : p.H0, off = i ? p.H0 : 0;

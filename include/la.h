@@ -601,8 +601,9 @@ LA_API la_status la_clear_outside(void* const* rows, const int* row_bytes, const
  * length). The first `rot` components are turned in pairs, pair i by
  * position * freqs[i] radians: (i, i + rot/2), or (2i, 2i + 1) if interleaved != 0:
  *   (a, b) -> (a cos - b sin, b cos + a sin).
- * An angle is position times a 64-bit fraction of a turn, not a float product: off by
- * less than 2^-31 of a turn at any position.
+ * An angle is position times a 64-bit fraction of a turn, not a float product: within
+ * 2^-31 of a turn at any position. Its sine and cosine are off by up to 2^-21 for bf16
+ * rows, by 2^-25 and 2^-22 of the value for fp32 rows.
  *
  * q, k      rows x[b,n,h,:] of d values at q + b q_stride[0] + n q_stride[1] + h
  *           q_stride[2] (k likewise; host arrays, in values, non-negative multiples of 16
