@@ -10,13 +10,9 @@
 //   4. O^T = scale e^G (Q S)^T + U^T P^T
 //   5. S^T = e^{G_C} S^T + (e^{G_C-G} U)^T K
 // Rows behind a sequence's last token are zeros in shared memory and have beta = 0.
-// A CTA is four warps of one head, which share the chunk's K, Q and triangles in two
-// buffers, the next chunk's copies in flight during a chunk (two warps a CTA: 278 us against
-// 229 for the backward of 64 heads of 4096 tokens, d = 128, and more at any other size).
-// Bound: forward, shared memory (each 16 x 16 block of K, Q, T, P is read for two
-// products of 16 cycles in all; 256 heads of 2048 tokens: 198 us, 227 with the copies by
-// cp.async; the tensor pipe has 56 % of it). Backward, the latency of a warp's way from product to
-// product, two warps to a sub-core: 215 us for 64 heads of 4096, the tensor pipe has 36 % of it.
+// A CTA is eight warps of one head (four for dv = 64), which share the chunk's K, Q and
+// triangles in two buffers, the next chunk's copies in flight during a chunk.
+// Bound: the latency of a warp's way from product to product, two warps to a sub-core.
 #include "la_gated_mma.cuh"
 
 namespace la {
@@ -32,20 +28,19 @@ using sm100::mbar_drain;
 using sm100::tma_load_3d;
 
 enum { kFwd = 0, kSave = 1, kRev = 2 };
-constexpr int W = 4;                                 // warps of a CTA
-
-template <int DK, int MODE, bool LO>
+// W: warps of a CTA
+template <int DK, int MODE, bool LO, int W>
 struct ChainSmem {
   static constexpr int KB = C * DK * 2;             // a tile of K or Q
   static constexpr int VB = C * W * 32;             // the CTA's columns of V or dO
-  // the part of the record that is wanted: [T lo | T hi | vec | P], [T hi | vec],
+  // the part of the record that is wanted: all, [T hi | vec],
   // [vec | T^T hi | P^T hi | T^T lo | P^T lo]
-  static constexpr int FROM = MODE == kFwd ? (LO ? 0 : FRAG) : MODE == kSave ? 0 : off_vec(true);
-  static constexpr int RB = MODE == kFwd ? REC_FWD - FROM : MODE == kSave ? off_rest(true) : VEC + (LO ? 4 : 2) * FRAG;
-  static constexpr int RV = MODE == kRev ? 0 : off_vec(MODE != kFwd) - FROM;          // vec in it
-  __host__ __device__ static constexpr int tri(int i) {   // T hi, T lo, P; reverse: T^T hi, T^T lo, P^T hi, P^T lo
+  static constexpr int FROM = MODE == kRev ? off_vec(true) : 0;
+  static constexpr int RB = MODE == kFwd ? REC_FWD : MODE == kSave ? off_rest(true) : VEC + (LO ? 4 : 2) * FRAG;
+  static constexpr int RV = MODE == kRev ? 0 : off_vec(MODE != kFwd);          // vec in it
+  __host__ __device__ static constexpr int tri(int i) {   // T hi, T lo, P hi, P lo (reverse: T^T, P^T)
     return MODE == kRev ? VEC + (i == 1 ? 2 : i == 2 ? 1 : i) * FRAG
-                        : i == 0 ? (MODE == kFwd ? FRAG - FROM : 0) : i == 1 ? 0 : RV + VEC;
+                        : i == 0 ? (MODE == kFwd ? FRAG : 0) : i == 1 ? 0 : RV + VEC + (i - 2) * FRAG;
   }
   static constexpr int K = 0;
   static constexpr int Q = K + KB;
@@ -75,9 +70,9 @@ struct ChainArgs {
 // Maps of [heads][rows][DK], of [heads][rows][dv], in boxes of 64 columns and 64 rows
 struct ChainMaps { CUtensorMap q, k, v; };
 
-template <int DK, int MODE, bool LO>
+template <int DK, int MODE, bool LO, int W>
 __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps, long long block, uint8_t* smem) {
-  using L = ChainSmem<DK, MODE, LO>;
+  using L = ChainSmem<DK, MODE, LO, W>;
   constexpr int NT = 32 * W, KS = DK / 16;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, ml = lane & 7;
@@ -113,7 +108,8 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
       tma_load_3d(to + L::K + x * C * 128, &maps.k, bar, 64 * x, t0, kh);
       if (MODE != kSave) tma_load_3d(to + L::Q + x * C * 128, &maps.q, bar, 64 * x, t0, kh);
     }
-    tma_load_3d(to + L::V, &maps.v, bar, blk * 16 * W, t0, vh);
+#pragma unroll
+    for (int x = 0; x < W / 4; ++x) tma_load_3d(to + L::V + x * C * 128, &maps.v, bar, blk * 16 * W + 64 * x, t0, vh);
     bulk_load(smem_addr(to) + L::R, p.rec + ((long long)(sq.slot + c) * p.H + h) * p.rec_bytes + L::FROM, L::RB, bar);
   };
   if (tid == 0 && nchunks > 0) load(0);
@@ -218,6 +214,11 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
           mma(y[2 * t], ah, bq[t][0], bq[t][1]);
           mma(y[2 * t + 1], ah, bq[t][2], bq[t][3]);
         }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          mma(y[2 * t], al, bq[t][0], bq[t][1]);
+          mma(y[2 * t + 1], al, bq[t][2], bq[t][3]);
+        }
       }
     }
 
@@ -257,14 +258,14 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
           mma(ev[2 * tb + 1], rh[jb], tl.z, tl.w);
         }
       // 4. U and the outputs
-      uint32_t u[4][4];
+      uint32_t u[4][4], ul[4][4];
       if (MODE == kFwd) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float2 b = *reinterpret_cast<const float2*>(BT + 8 * j + 2 * tig);
           const float2 eg = *reinterpret_cast<const float2*>(EG + 8 * j + 2 * tig);
-          u[j >> 1][2 * (j & 1)] = pack2(b.x * ev[j][0], b.y * ev[j][1]);
-          u[j >> 1][2 * (j & 1) + 1] = pack2(b.x * ev[j][2], b.y * ev[j][3]);
+          split2(b.x * ev[j][0], b.y * ev[j][1], u[j >> 1][2 * (j & 1)], ul[j >> 1][2 * (j & 1)]);
+          split2(b.x * ev[j][2], b.y * ev[j][3], u[j >> 1][2 * (j & 1) + 1], ul[j >> 1][2 * (j & 1) + 1]);
           y[j][0] *= p.scale * eg.x; y[j][1] *= p.scale * eg.y;
           y[j][2] *= p.scale * eg.x; y[j][3] *= p.scale * eg.y;
         }
@@ -272,9 +273,13 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
         for (int jb = 0; jb < 4; ++jb)
 #pragma unroll
           for (int tb = jb; tb < 4; ++tb) {
-            const uint4 w = frag(2, block_of(tb, jb));
+            const uint4 w = frag(2, block_of(tb, jb)), wl = frag(3, block_of(tb, jb));
             mma(y[2 * tb], u[jb], w.x, w.y);
             mma(y[2 * tb + 1], u[jb], w.z, w.w);
+            mma(y[2 * tb], ul[jb], w.x, w.y);
+            mma(y[2 * tb + 1], ul[jb], w.z, w.w);
+            mma(y[2 * tb], u[jb], wl.x, wl.y);
+            mma(y[2 * tb + 1], u[jb], wl.z, wl.w);
           }
         // A zero weight of a later token's row that is not finite would be NaN
         // for the tokens before it: such a chunk is done again, each token
@@ -316,8 +321,8 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float2 b = *reinterpret_cast<const float2*>(BT + 8 * j + 2 * tig);
-            u[j >> 1][2 * (j & 1)] = pack2(b.x * ev[j][0], b.y * ev[j][1]);
-            u[j >> 1][2 * (j & 1) + 1] = pack2(b.x * ev[j][2], b.y * ev[j][3]);
+            split2(b.x * ev[j][0], b.y * ev[j][1], u[j >> 1][2 * (j & 1)], ul[j >> 1][2 * (j & 1)]);
+            split2(b.x * ev[j][2], b.y * ev[j][3], u[j >> 1][2 * (j & 1) + 1], ul[j >> 1][2 * (j & 1) + 1]);
           }
           // (Q S)^T again: a product of the state's columns with one query's row
           float qs[8][4];
@@ -337,6 +342,8 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
               ldmatrix4(b, sb + L::Q + box_at(16 * t + ((mi >> 1) << 3) + ml, 2 * ks + (mi & 1)));
               mma(qs[2 * t], ah, b[0], b[1]);
               mma(qs[2 * t + 1], ah, b[2], b[3]);
+              mma(qs[2 * t], al, b[0], b[1]);
+              mma(qs[2 * t + 1], al, b[2], b[3]);
             }
           }
 #pragma unroll 1
@@ -352,15 +359,16 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
 #pragma unroll
             for (int jb = 0; jb < 4; ++jb) {
               if (jb > tb) continue;
-              uint32_t a[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int j = 16 * jb + 8 * (e >> 1) + 2 * tig;
-                a[e] = u[jb][e] & ((j <= t ? 0xffffu : 0u) | (j + 1 <= t ? 0xffff0000u : 0u));
-              }
-              const uint4 w = frag(2, block_of(tb, jb));
+              uint32_t a[4], b[4];
+              rows_to(a, u[jb], jb, t, tig);
+              rows_to(b, ul[jb], jb, t, tig);
+              const uint4 w = frag(2, block_of(tb, jb)), wl = frag(3, block_of(tb, jb));
               mma(o2[0], a, w.x, w.y);
               mma(o2[1], a, w.z, w.w);
+              mma(o2[0], b, w.x, w.y);
+              mma(o2[1], b, w.z, w.w);
+              mma(o2[0], a, wl.x, wl.y);
+              mma(o2[1], a, wl.z, wl.w);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -529,28 +537,29 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
   }
 }
 
-template <int DK, bool LO>
+template <int DK, int W>
 __global__ void __launch_bounds__(32 * W)
 gated_chain_kernel(const ChainArgs p, const __grid_constant__ ChainMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  chain<DK, kFwd, LO>(p, maps, blockIdx.x, smem);
+  chain<DK, kFwd, true, W>(p, maps, blockIdx.x, smem);
 }
 
 // Both chains of the backward in one launch (they need nothing of each other; order:
 // second_chain). The states before the chunks are kept as bf16 whatever is
 // asked for: that chain takes operands rounded once.
-template <int DK, bool LO>
+template <int DK, bool LO, int W>
 __global__ void __launch_bounds__(32 * W)
 gated_chains_kernel(const ChainArgs rev, const __grid_constant__ ChainMaps rmaps, const ChainArgs save,
                     const __grid_constant__ ChainMaps smaps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   unsigned number;
-  if (second_chain(blockIdx.x, gridDim.x, rev.offsets != nullptr, rev.nblk * rev.H, number)) chain<DK, kSave, false>(save, smaps, number, smem);
-  else chain<DK, kRev, LO>(rev, rmaps, number, smem);
+  if (second_chain(blockIdx.x, gridDim.x, rev.offsets != nullptr, rev.nblk * rev.H, number)) chain<DK, kSave, false, W>(save, smaps, number, smem);
+  else chain<DK, kRev, LO, W>(rev, rmaps, number, smem);
 }
 
-template <int DK, bool LO>
+template <int DK, bool LO, int W>
 cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
+  f.nblk = a.dv / (16 * W);
   const long long grid = (long long)f.nseq * f.H * f.nblk * (save != nullptr ? 2 : 1);
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const long long keys = (long long)a.B * a.Hk, heads = (long long)a.B * a.H;
@@ -562,20 +571,21 @@ cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
   f.stall = take_gated_timeout_test(0) ? 1 : 0;
   cudaError_t e;
   if (save == nullptr) {
-    auto kern = gated_chain_kernel<DK, LO>;
-    const int smem = ChainSmem<DK, kFwd, LO>::TOTAL;
+    auto kern = gated_chain_kernel<DK, W>;
+    const int smem = ChainSmem<DK, kFwd, true, W>::TOTAL;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, 32 * W, smem, a.stream>>>(f, m);
   } else {
     ChainArgs b = *save;
+    b.nblk = f.nblk;
     b.status = f.status;
     b.stall = f.stall;
     ms = m;
     if (!gated_map(&ms.v, b.v, heads, a.N, a.dv, 64)) return cudaErrorInvalidValue;
-    auto kern = gated_chains_kernel<DK, LO>;
-    constexpr int smem = ChainSmem<DK, kRev, LO>::TOTAL;
-    static_assert(smem >= ChainSmem<DK, kSave, false>::TOTAL, "the reverse chain has more");
+    auto kern = gated_chains_kernel<DK, LO, W>;
+    constexpr int smem = ChainSmem<DK, kRev, LO, W>::TOTAL;
+    static_assert(smem >= ChainSmem<DK, kSave, false, W>::TOTAL, "the reverse chain has more");
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, 32 * W, smem, a.stream>>>(f, m, b, ms);
@@ -586,15 +596,16 @@ cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
 }
 
 cudaError_t dispatch(const GatedArgs& a, const ChainArgs& f, const ChainArgs* save) {
-  const bool lo = f.S_out != nullptr;
-  if (a.dk == 64) return lo ? launch<64, true>(a, f, save) : launch<64, false>(a, f, save);
-  return lo ? launch<128, true>(a, f, save) : launch<128, false>(a, f, save);
+  const bool lo = save == nullptr || f.S_out != nullptr;
+  if (save == nullptr && a.dv == 128) return a.dk == 64 ? launch<64, true, 8>(a, f, save) : launch<128, true, 8>(a, f, save);
+  if (a.dk == 64) return lo ? launch<64, true, 4>(a, f, save) : launch<64, false, 4>(a, f, save);
+  return lo ? launch<128, true, 4>(a, f, save) : launch<128, false, 4>(a, f, save);
 }
 
 ChainArgs chain_args(const GatedArgs& a, const uint8_t* rec, int rec_bytes) {
   ChainArgs p{};
   p.v = a.v; p.rec = rec; p.rec_bytes = rec_bytes; p.offsets = a.offsets;
-  p.Hk = a.Hk; p.H = a.H; p.N = a.N; p.dv = a.dv; p.nseq = a.nseq; p.nblk = a.dv / (16 * W); p.scale = a.scale;
+  p.Hk = a.Hk; p.H = a.H; p.N = a.N; p.dv = a.dv; p.nseq = a.nseq; p.scale = a.scale;
   return p;
 }
 

@@ -540,7 +540,7 @@ size_t mma_gated_backward_workspace(int B, int H, int N, int dk, int dv, int nse
 }
 
 cudaError_t mma_gated_forward(const GatedArgs& a) {
-  const cudaError_t e = gated_prep(a, (uint8_t*)a.workspace, nullptr, a.S_final != nullptr);
+  const cudaError_t e = gated_prep(a, (uint8_t*)a.workspace, nullptr, true);
   if (e != cudaSuccess) return e;
   const uint8_t* records = (const uint8_t*)a.workspace;
   if (gated_split_wanted(a, false)) return gated_split_forward(a, records);

@@ -20,13 +20,13 @@
 // keeps its tensor pipe busy: 8 cycles an instruction (measured: 595 TFLOP/s
 // on 152 SMs, the same with 1, 2 and 4 warps a sub-core).
 //
-// Precision: fp32 operands that reach a state that the caller gets go in as bf16
-// high and low parts (lo lo is left out: a product is off by 2^-15 of itself at most,
-// 2^-18 as a root mean square); q, k, v, dO are bf16 as they are. What only reaches
-// rows that are rounded to bf16 anyway goes in rounded once: S in the read Q S, P and
-// U in P U, and, where no state is asked for, every operand (232 products of 16 x 8 x 16
-// a chunk and 16 columns in the place of 400, which the tensor pipe is bound by); the state itself,
-// its sums and decays stay fp32 in every case.
+// Precision: fp32 operands go in as bf16 high and low parts (lo lo is left out: a
+// product is off by 2^-15 of itself at most, 2^-18 as a root mean square); q, k, v, dO
+// are bf16 as they are; the state itself, its sums and decays are fp32. Rounding what only
+// reaches rows of bf16 once would take 232 products of 16 x 8 x 16 a chunk and 16 columns (d = 128)
+// in the place of 504, but R, the triangles and the sums over them cancel where keys are
+// alike: with cosines of 0.9 between them outputs were off by up to 2e-2 of their two-norm (3.4e-3
+// with independent keys). In the backward what reaches no dS0 goes in rounded once still.
 #pragma once
 
 #include "la_gated.cuh"
@@ -46,9 +46,9 @@ constexpr int C = 64;                      // tokens per chunk
 constexpr int NB = 10;                     // 16 x 16 blocks on and below the diagonal
 constexpr int FRAG = NB * 512;             // bytes of a triangle's B fragments, bf16
 constexpr int VEC = 3 * C * 4;             // e^G, e^{G_C - G}, beta
-// A chunk's record: forward [T lo | T hi | vec | P]; backward [T hi | vec | T^T hi |
+// A chunk's record: forward [T lo | T hi | vec | P hi | P lo]; backward [T hi | vec | T^T hi |
 // P^T hi | T^T lo | P^T lo | G / log 2 as two fp32].
-constexpr int REC_FWD = 3 * FRAG + VEC;
+constexpr int REC_FWD = 4 * FRAG + VEC;
 constexpr int REC_BWD = 5 * FRAG + VEC + 2 * C * 4;
 __host__ __device__ constexpr int off_vec(bool backward) { return backward ? FRAG : 2 * FRAG; }
 __host__ __device__ constexpr int off_rest(bool backward) { return off_vec(backward) + VEC; }

@@ -39,25 +39,24 @@ using sm100::tma_load_3d;
 
 constexpr int W = 4;                                 // pairs of a CTA
 
-template <int DK, bool LO>
+template <int DK>
 struct PairSmem {
   static constexpr int TB = C * DK * 2;              // a tile of K or Q
-  // for the chain: K, the CTA's columns of V, [T lo | T hi | vec] or [T hi | vec]
-  static constexpr int FROM = LO ? 0 : FRAG;
+  // for the chain: K, the CTA's columns of V, [T lo | T hi | vec]
   static constexpr int V = TB;
   static constexpr int R = V + C * W * 32;
-  static constexpr int VA = off_vec(false) - FROM;   // vec in it
+  static constexpr int VA = off_vec(false);          // vec in it
   static constexpr int RA = VA + VEC;
   static constexpr int up(int x) { return (x + 1023) / 1024 * 1024; }   // (the swizzle goes by the address)
   static constexpr int A_BYTES = R + RA, A = up(A_BYTES);
-  // for the helpers: Q, [vec | P]
-  static constexpr int RB = VEC + FRAG;
+  // for the helpers: Q, [vec | P hi | P lo]
+  static constexpr int RB = VEC + 2 * FRAG;
   static constexpr int B_BYTES = TB + RB, B = up(B_BYTES);
-  // from a chain warp to its helper, two chunks': S^T's fragments, U's
+  // from a chain warp to its helper, two chunks': S^T's fragments, high and low, U's
   static constexpr int SF = DK / 16 * 512;
-  static constexpr int X = SF + 4 * 512;
-  static constexpr int AT_B = 3 * A, AT_X = AT_B + 3 * B;
-  static constexpr int BARS = AT_X + 2 * W * X;      // four barriers, a flag
+  static constexpr int X = 2 * SF + 2 * 4 * 512;
+  static constexpr int AT_B = 2 * A, AT_X = AT_B + 2 * B;
+  static constexpr int BARS = AT_X + 2 * W * X;      // two barriers, a flag
   static constexpr int TOTAL = BARS + 64;
   static_assert(TOTAL <= 227 * 1024 && SF >= C * 32, "shared memory");
 };
@@ -76,11 +75,11 @@ struct PairArgs {
 // Maps of [heads][rows][DK], of [heads][rows][dv], in boxes of 64 columns and 64 rows
 struct PairMaps { CUtensorMap q, k, v; };
 
-template <int DK, bool LO>
+template <int DK>
 __global__ void __launch_bounds__(64 * W, 1)
 gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  using L = PairSmem<DK, LO>;
+  using L = PairSmem<DK>;
   constexpr int NT = 32 * W, KS = DK / 16;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & (W - 1);
   const bool helper = threadIdx.x >= NT;
@@ -98,7 +97,7 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
   volatile int* gave_up = reinterpret_cast<volatile int*>(smem + L::BARS + 32);
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[i], 1);
     *gave_up = 0;
     fence_mbar_init();
   }
@@ -108,25 +107,25 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
     const int kh = sq.b * p.Hk + h / (p.H / p.Hk), vh = sq.b * p.H + h;
     const long long vrow = (long long)vh * p.N + sq.lo;
     const uint8_t* rec = p.rec + ((long long)sq.slot * p.H + h) * REC_FWD;
-    // One thread asks for copies, in turn i: chunk i + 2 for the chain, whose buffer
-    // chunk i - 1 had, and chunk i + 1 for the helpers, who are at chunk i - 1. They have
-    // landed at turn i + 2's barrier; turns take four barriers one after the other.
+    // One thread asks for copies, in turn i: chunk i + 1 for the chain, whose buffer chunk
+    // i - 1 had, and chunk i for the helpers, who are at chunk i - 1. They have landed at
+    // turn i + 1's barrier; turns take two barriers one after the other.
     auto load = [&](int i) {
-      const bool a = i + 2 < nchunks, b = i + 1 >= 0 && i + 1 < nchunks;
-      uint64_t* bar = &bars[(i + 2) & 3];
-      mbar_arrive_expect_tx(bar, (a ? L::A_BYTES : 0) + (b ? L::B_BYTES : 0) + (p.stall && i == -2 ? 16 : 0));
+      const bool a = i + 1 < nchunks, b = i >= 0 && i < nchunks;
+      uint64_t* bar = &bars[(i + 1) & 1];
+      mbar_arrive_expect_tx(bar, (a ? L::A_BYTES : 0) + (b ? L::B_BYTES : 0) + (p.stall && i == -1 ? 16 : 0));
       if (a) {
-        const int c = i + 2, t0 = sq.lo + c * C, at = c % 3 * L::A;
+        const int c = i + 1, t0 = sq.lo + c * C, at = (c & 1) * L::A;
 #pragma unroll
         for (int x = 0; x < DK / 64; ++x) tma_load_3d(smem + at + x * C * 128, &maps.k, bar, 64 * x, t0, kh);
         tma_load_3d(smem + at + L::V, &maps.v, bar, blk * 16 * W, t0, vh);
-        bulk_load(base + at + L::R, rec + (long long)c * p.H * REC_FWD + L::FROM, L::RA, bar);
+        bulk_load(base + at + L::R, rec + (long long)c * p.H * REC_FWD, L::RA, bar);
       }
       if (b) {
-        const int c = i + 1, t0 = sq.lo + c * C, at = L::AT_B + c % 3 * L::B;
+        const int t0 = sq.lo + i * C, at = L::AT_B + (i & 1) * L::B;
 #pragma unroll
         for (int x = 0; x < DK / 64; ++x) tma_load_3d(smem + at + x * C * 128, &maps.q, bar, 64 * x, t0, kh);
-        bulk_load(base + at + L::TB, rec + (long long)c * p.H * REC_FWD + off_vec(false), L::RB, bar);
+        bulk_load(base + at + L::TB, rec + (long long)i * p.H * REC_FWD + off_vec(false), L::RB, bar);
       }
     };
     // Copies have whole boxes: rows behind the sequence's last token become zeros.
@@ -137,37 +136,35 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
     };
     bool ok = true;                                  // (once a wait gave up, none is begun and no copy asked for)
     int late = 0;
-    if (tid == 0) {
-      load(-2);
-      load(-1);
-    }
+    if (tid == 0) load(-1);
     __nv_bfloat16* ob = p.out + vrow * p.dv + m0;
     for (int i = 0; i <= nchunks; ++i) {
       if (ok) {
-        ok = mbar_drain(&bars[i & 3], (i >> 2) & 1, kWaitNs);
+        ok = mbar_drain(&bars[i & 1], (i >> 1) & 1, kWaitNs);
         late = i;
         if (!ok) *gave_up = 1;
       }
-      if (n % C != 0 && i == nchunks - 1) clear(i % 3 * L::A, DK / 64 + 1);        // K and V
-      if (n % C != 0 && i == nchunks) clear(L::AT_B + (i - 1) % 3 * L::B, DK / 64);
+      if (n % C != 0 && i == nchunks - 1) clear((i & 1) * L::A, DK / 64 + 1);        // K and V
+      if (n % C != 0 && i == nchunks) clear(L::AT_B + ((i - 1) & 1) * L::B, DK / 64);
       __syncthreads();                               // chunk i's copies are there, chunk i - 1's chain is done
       if (tid == 0 && ok) load(i);
       if (i == 0) continue;
       const int c = i - 1, t0 = c * C, cn = min(C, n - t0);
-      const uint32_t sb = base + L::AT_B + c % 3 * L::B;
-      const uint8_t* rp = smem + L::AT_B + c % 3 * L::B + L::TB;
+      const uint32_t sb = base + L::AT_B + (c & 1) * L::B;
+      const uint8_t* rp = smem + L::AT_B + (c & 1) * L::B + L::TB;
       const float* EG = reinterpret_cast<const float*>(rp);
       uint8_t* xp = smem + L::AT_X + ((c & 1) * W + warp) * L::X;
-      auto pfrag = [&](int b) { return *reinterpret_cast<const uint4*>(rp + VEC + b * 512 + lane * 16); };
+      auto pfrag = [&](int lo, int b) { return *reinterpret_cast<const uint4*>(rp + VEC + lo * FRAG + b * 512 + lane * 16); };
       auto product = [&](float (&y)[8][4]) {         // (Q S)^T
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[j][e] = 0.f;
-        uint4 a[2];
+        uint4 a[2], d[2];                            // high and low parts
         uint32_t b[2][4][4];
         auto ask = [&](int ks) {
           a[ks & 1] = *reinterpret_cast<const uint4*>(xp + ks * 512 + lane * 16);
+          d[ks & 1] = *reinterpret_cast<const uint4*>(xp + L::SF + ks * 512 + lane * 16);
 #pragma unroll
           for (int t = 0; t < 4; ++t)
             ldmatrix4(b[ks & 1][t], sb + box_at(16 * t + ((mi >> 1) << 3) + ml, 2 * ks + (mi & 1)));
@@ -182,18 +179,26 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
             mma(y[2 * t], w, b[ks & 1][t][0], b[ks & 1][t][1]);
             mma(y[2 * t + 1], w, b[ks & 1][t][2], b[ks & 1][t][3]);
           }
+          const uint32_t wl[4] = {d[ks & 1].x, d[ks & 1].y, d[ks & 1].z, d[ks & 1].w};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            mma(y[2 * t], wl, b[ks & 1][t][0], b[ks & 1][t][1]);
+            mma(y[2 * t + 1], wl, b[ks & 1][t][2], b[ks & 1][t][3]);
+          }
         }
       };
       float y[8][4];
       product(y);
       uint4 pf[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) pf[b] = pfrag(b);
-      uint32_t u[4][4];
+      for (int b = 0; b < NB; ++b) pf[b] = pfrag(0, b);
+      uint32_t u[4][4], ul[4][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint4 w = *reinterpret_cast<const uint4*>(xp + L::SF + t * 512 + lane * 16);
+        const uint4 w = *reinterpret_cast<const uint4*>(xp + 2 * L::SF + t * 512 + lane * 16);
+        const uint4 l = *reinterpret_cast<const uint4*>(xp + 2 * L::SF + 2048 + t * 512 + lane * 16);
         u[t][0] = w.x; u[t][1] = w.y; u[t][2] = w.z; u[t][3] = w.w;
+        ul[t][0] = l.x; ul[t][1] = l.y; ul[t][2] = l.z; ul[t][3] = l.w;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -205,9 +210,13 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
       for (int jb = 0; jb < 4; ++jb)
 #pragma unroll
         for (int tb = jb; tb < 4; ++tb) {
-          const uint4 w = pf[block_of(tb, jb)];
+          const uint4 w = pf[block_of(tb, jb)], wl = pfrag(1, block_of(tb, jb));
           mma(y[2 * tb], u[jb], w.x, w.y);
           mma(y[2 * tb + 1], u[jb], w.z, w.w);
+          mma(y[2 * tb], ul[jb], w.x, w.y);
+          mma(y[2 * tb + 1], ul[jb], w.z, w.w);
+          mma(y[2 * tb], u[jb], wl.x, wl.y);
+          mma(y[2 * tb + 1], u[jb], wl.z, wl.w);
         }
       // A zero weight of a later token's row that is not finite would be NaN
       // for the tokens before it: such a chunk is done again, each token
@@ -228,11 +237,16 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
 #pragma unroll
           for (int jb = 0; jb < 4; ++jb) {
             if (jb > tb) continue;
-            uint32_t a[4];
+            uint32_t a[4], b[4];
             rows_to(a, u[jb], jb, t, tig);
-            const uint4 w = pfrag(block_of(tb, jb));
+            rows_to(b, ul[jb], jb, t, tig);
+            const uint4 w = pfrag(0, block_of(tb, jb)), wl = pfrag(1, block_of(tb, jb));
             mma(o2[0], a, w.x, w.y);
             mma(o2[1], a, w.z, w.w);
+            mma(o2[0], b, w.x, w.y);
+            mma(o2[1], b, w.z, w.w);
+            mma(o2[0], a, wl.x, wl.y);
+            mma(o2[1], a, wl.z, wl.w);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -259,7 +273,7 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
       }
     }
     if (!ok) {
-      for (int q = late; q < late + 2; ++q) mbar_drain(&bars[q & 3], (q >> 2) & 1, kWaitNs / 8);
+      mbar_drain(&bars[late & 1], (late >> 1) & 1, kWaitNs / 8);
       atomicExch(p.status, (int)LA_ERR_TIMEOUT);      // (any thread's: one may give up where the others just did not)
     }
     return;
@@ -277,14 +291,14 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
   __syncthreads();
   for (int i = 0; i < nchunks; ++i) {
     const int cn = min(C, n - i * C);
-    const uint32_t sb = base + i % 3 * L::A;
-    const uint8_t* rp = smem + i % 3 * L::A + L::R;
+    const uint32_t sb = base + (i & 1) * L::A;
+    const uint8_t* rp = smem + (i & 1) * L::A + L::R;
     const float* EG = reinterpret_cast<const float*>(rp + L::VA);
     const float* EC = EG + C;
     const float* BT = EG + 2 * C;
     uint8_t* xp = smem + L::AT_X + ((i & 1) * W + warp) * L::X;
     auto tfrag = [&](bool low, int b) {
-      return *reinterpret_cast<const uint4*>(rp + (LO && !low ? FRAG : 0) + b * 512 + lane * 16);
+      return *reinterpret_cast<const uint4*>(rp + (low ? 0 : FRAG) + b * 512 + lane * 16);
     };
     // 1. (K S)^T (fragments are asked for ahead of the stores, which no load may pass)
     float x[8][4];
@@ -310,18 +324,17 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
       split2(st[2 * ks + 1][0], st[2 * ks + 1][1], ah[2], al[2]);
       split2(st[2 * ks + 1][2], st[2 * ks + 1][3], ah[3], al[3]);
       *reinterpret_cast<uint4*>(xp + ks * 512 + lane * 16) = make_uint4(ah[0], ah[1], ah[2], ah[3]);
+      *reinterpret_cast<uint4*>(xp + L::SF + ks * 512 + lane * 16) = make_uint4(al[0], al[1], al[2], al[3]);
       const uint32_t (&b)[4][4] = kb[ks & 1];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         mma(x[2 * t], ah, b[t][0], b[t][1]);
         mma(x[2 * t + 1], ah, b[t][2], b[t][3]);
       }
-      if (LO) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          mma(x[2 * t], al, b[t][0], b[t][1]);
-          mma(x[2 * t + 1], al, b[t][2], b[t][3]);
-        }
+      for (int t = 0; t < 4; ++t) {
+        mma(x[2 * t], al, b[t][0], b[t][1]);
+        mma(x[2 * t + 1], al, b[t][2], b[t][3]);
       }
     }
     const float last = EG[C - 1];
@@ -349,7 +362,6 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
         const uint4 th = tfrag(false, block_of(tb, jb));
         mma(ev[2 * tb], rh[jb], th.x, th.y);
         mma(ev[2 * tb + 1], rh[jb], th.z, th.w);
-        if (!LO) continue;
         const uint4 tl = tfrag(true, block_of(tb, jb));
         mma(ev[2 * tb], rl[jb], th.x, th.y);
         mma(ev[2 * tb + 1], rl[jb], th.z, th.w);
@@ -369,7 +381,6 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
           rows_to(b, rl[jb], jb, t, tig);
           const uint4 th = tfrag(false, block_of(tb, jb));
           mma(e2[0], a, th.x, th.y); mma(e2[1], a, th.z, th.w);
-          if (!LO) continue;
           const uint4 tl = tfrag(true, block_of(tb, jb));
           mma(e2[0], b, th.x, th.y); mma(e2[1], b, th.z, th.w);
           mma(e2[0], a, tl.x, tl.y); mma(e2[1], a, tl.z, tl.w);
@@ -392,16 +403,17 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
     uint32_t uh[4][4], ul[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      uint32_t u[4];
+      uint32_t u[4], u2[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = 2 * t + (e >> 1), r = 2 * (e & 1);
         const float2 b = *reinterpret_cast<const float2*>(BT + 8 * j + 2 * tig);
         const float2 ec = *reinterpret_cast<const float2*>(EC + 8 * j + 2 * tig);
-        u[e] = pack2(b.x * ev[j][r], b.y * ev[j][r + 1]);
+        split2(b.x * ev[j][r], b.y * ev[j][r + 1], u[e], u2[e]);
         split2(b.x * ec.x * ev[j][r], b.y * ec.y * ev[j][r + 1], uh[t][e], ul[t][e]);
       }
-      *reinterpret_cast<uint4*>(xp + L::SF + t * 512 + lane * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<uint4*>(xp + 2 * L::SF + t * 512 + lane * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<uint4*>(xp + 2 * L::SF + 2048 + t * 512 + lane * 16) = make_uint4(u2[0], u2[1], u2[2], u2[3]);
     }
     // 4. S^T
 #pragma unroll
@@ -416,12 +428,10 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
         mma(st[2 * k2], uh[t], kt[t & 1][k2][0], kt[t & 1][k2][1]);
         mma(st[2 * k2 + 1], uh[t], kt[t & 1][k2][2], kt[t & 1][k2][3]);
       }
-      if (LO) {
 #pragma unroll
-        for (int k2 = 0; k2 < KS; ++k2) {
-          mma(st[2 * k2], ul[t], kt[t & 1][k2][0], kt[t & 1][k2][1]);
-          mma(st[2 * k2 + 1], ul[t], kt[t & 1][k2][2], kt[t & 1][k2][3]);
-        }
+      for (int k2 = 0; k2 < KS; ++k2) {
+        mma(st[2 * k2], ul[t], kt[t & 1][k2][0], kt[t & 1][k2][1]);
+        mma(st[2 * k2 + 1], ul[t], kt[t & 1][k2][2], kt[t & 1][k2][3]);
       }
     }
     __syncthreads();                                 // the helper has this chunk, the next one's copies are there
@@ -435,12 +445,12 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
   }
 }
 
-template <int DK, bool LO>
+template <int DK>
 cudaError_t launch(PairArgs p, const PairMaps& maps, cudaStream_t stream) {
   const long long grid = (long long)p.nseq * p.H * p.nblk;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  auto kern = gated_pair_kernel<DK, LO>;
-  const int smem = PairSmem<DK, LO>::TOTAL;
+  auto kern = gated_pair_kernel<DK>;
+  const int smem = PairSmem<DK>::TOTAL;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)grid, 64 * W, smem, stream>>>(p, maps);
@@ -471,8 +481,7 @@ cudaError_t gated_pair_forward(const GatedArgs& a, const uint8_t* records) {
   p.stall = take_gated_timeout_test(0) ? 1 : 0;
   p.rec = records; p.offsets = a.offsets; p.S_in = a.S0; p.S_out = a.S_final; p.out = (__nv_bfloat16*)a.out;
   p.Hk = a.Hk; p.H = a.H; p.N = a.N; p.dv = a.dv; p.nseq = a.nseq; p.nblk = a.dv / (16 * W); p.scale = a.scale;
-  if (a.dk == 64) return p.S_out != nullptr ? launch<64, true>(p, maps, a.stream) : launch<64, false>(p, maps, a.stream);
-  return p.S_out != nullptr ? launch<128, true>(p, maps, a.stream) : launch<128, false>(p, maps, a.stream);
+  return a.dk == 64 ? launch<64>(p, maps, a.stream) : launch<128>(p, maps, a.stream);
 }
 
 }  // namespace la

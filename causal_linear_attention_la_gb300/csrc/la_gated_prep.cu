@@ -56,7 +56,7 @@ struct PrepArgs {
   int4* chunks;                       // backward
   int Hk, H, N, nseq;
   float scale;
-  int lo;                             // low parts of T (backward: of T^T and P^T) wanted
+  int lo;                             // backward: low parts of T^T and P^T wanted
 };
 
 // Four values of a 16 x 16 block as the B fragments of its two 8-column tiles.
@@ -243,7 +243,7 @@ gated_prep_kernel(const PrepArgs p) {
     // it rounded once), and for the backward pairs of rows of a column
     auto store_t = [&](int block, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
       store_frag(rec + (kBackward ? 0 : FRAG), block, lane, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      if (!kBackward && p.lo) store_frag(rec, block, lane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      if (!kBackward) store_frag(rec, block, lane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       if (kBackward) {
         store_frag(rec + off_rest(true), block, lane, make_uint4(transposed(hi[0]), transposed(hi[2]), transposed(hi[1]), transposed(hi[3])));
         if (p.lo)
@@ -258,7 +258,7 @@ gated_prep_kernel(const PrepArgs p) {
     // X diag(beta): into sm.a on the diagonal, kept as fragments (pairs of columns) below
     uint32_t bh[6][2], bl[6][2];           // tiles 0 .. 3 (warps 2, 3) and the block beside the diagonal (1, 3); rows g, g + 8
     auto block = [&](int jb, auto diagonal) {
-      uint32_t w[4];
+      uint32_t w[4], wl[4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int tile = 2 * jb + half, j = 8 * tile + 2 * tig;
@@ -284,10 +284,13 @@ gated_prep_kernel(const PrepArgs p) {
             const int at = jb == warp - 1 && (warp & 1) ? 4 + half : tile & 3;
             split2(d0 * kk[tile][2 * r] * bj.x, d1 * kk[tile][2 * r + 1] * bj.y, bh[at][r], bl[at][r]);
           }
-          if (!kBackward) w[2 * r + half] = pack2(p0, p1);
+          if (!kBackward) split2(p0, p1, w[2 * r + half], wl[2 * r + half]);
         }
       }
-      if (!kBackward) store_frag(rec + off_rest(false), block_of(warp, jb), lane, make_uint4(w[0], w[1], w[2], w[3]));
+      if (!kBackward) {
+        store_frag(rec + off_rest(false), block_of(warp, jb), lane, make_uint4(w[0], w[1], w[2], w[3]));
+        store_frag(rec + off_rest(false) + FRAG, block_of(warp, jb), lane, make_uint4(wl[0], wl[1], wl[2], wl[3]));
+      }
     };
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {

@@ -14,7 +14,7 @@
 // Four helper warps do what the chain need not wait for: the copies of later
 // chunks by TMA (by cp.async their 100 instructions a chunk took 1300 cycles, more than
 // half of the chain's time), (Q S)^T + U^T P^T and the outputs of the chunk before (a chain warp leaves its
-// split S as fragments), in the backward P^T dO and the states that are kept. One
+// split S and U as fragments), in the backward P^T dO and the states that are kept. One
 // barrier of all eight warps a chunk, two of the chain warps alone.
 #include <cudaTypedefs.h>
 
@@ -41,22 +41,23 @@ struct SplitSmem {
   static constexpr int VB = C * 32;                  // 16 columns of V or dO
   static constexpr int up(int x) { return (x + 1023) / 1024 * 1024; }   // (the swizzle goes by the address)
   // copies for the chain: K, (forward: V, backward: Q), T's triangles, vec
-  static constexpr int TRI = (LO ? 2 : 1) * FRAG;
+  static constexpr int TRI = (LO ? 2 : 1) * FRAG;    // (forward: LO)
   static constexpr int A_X = TB;                     // V or Q
   static constexpr int A_T = A_X + (MODE == kRev ? TB : VB);
   static constexpr int A_VEC = A_T + (MODE == kSave ? FRAG : TRI);
   static constexpr int A_BYTES = A_VEC + VEC, A = up(A_BYTES);
   // and for the helpers: Q and P; backward dO and P^T's triangles; vec
   static constexpr int B_P = MODE == kRev ? VB : TB;
-  static constexpr int B_VEC = B_P + (MODE == kRev ? TRI : FRAG);
+  static constexpr int B_VEC = B_P + TRI;
   static constexpr int B_BYTES = MODE == kSave ? 0 : B_VEC + VEC, B = up(B_BYTES);
   // between the warps
   static constexpr int SHARES = 0;                   // [to][from, without itself][2 tiles][lane] float4
   static constexpr int FR = SHARES + 12 * 1024;      // R's fragments [block][hi, lo][lane] 16 bytes
   static constexpr int FU = FR + 4096;               // and those of e^{G_C-G} U, or -e^G dR
-  static constexpr int ROWS = FU + 4096;             // two chunks' U, E or dR, rounded, and outputs on their way
-  static constexpr int SF = ROWS + 2 * 2048;         // two chunks' S^T: [hi, lo][DK / 16][lane] 16 bytes
-  static constexpr int SFB = (MODE == kFwd ? 1 : 2) * (DK / 16) * 512;
+  static constexpr int ROWS = FU + 4096;             // two chunks' U [hi, lo][block][lane] 16 bytes, or E or dR, rounded
+  static constexpr int ROWB = MODE == kFwd ? 4096 : 2048;
+  static constexpr int SF = ROWS + 2 * ROWB;         // two chunks' S^T: [hi, lo][DK / 16][lane] 16 bytes
+  static constexpr int SFB = 2 * (DK / 16) * 512;
   static constexpr int PRE = SF + 2 * SFB;           // backward, three chunks': P^T dO [block][2][lane] float4,
   static constexpr int PREB = MODE == kRev ? 4096 + 4096 : 0;   // fragments of scale e^G dO
   static constexpr int OUT = PRE + 3 * PREB;         // helper warps' rows on their way out
@@ -136,7 +137,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       else tma_load_3d(smem + (to - base) + L::A_X, &maps.v, bar, m0, sq.lo + t0, vh);
       const uint8_t* rec = p.rec + ((long long)(sq.slot + c) * p.H + h) * p.rec_bytes;
       if (MODE == kFwd) {                            // [T lo | T hi | vec]
-        bulk_load(to + L::A_T, rec + (LO ? 0 : FRAG), L::TRI + VEC, bar);
+        bulk_load(to + L::A_T, rec, L::TRI + VEC, bar);
       } else if (MODE == kSave) {                    // [T hi | vec]
         bulk_load(to + L::A_T, rec, FRAG + VEC, bar);
       } else {                                       // T^T hi, T^T lo, vec
@@ -152,7 +153,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       const uint8_t* rec = p.rec + ((long long)(sq.slot + c) * p.H + h) * p.rec_bytes;
       if (MODE == kFwd) {
         boxes(to, &maps.q, t0, bar);
-        bulk_load(to + L::B_P, rec + off_rest(false), FRAG, bar);
+        bulk_load(to + L::B_P, rec + off_rest(false), L::TRI, bar);
       } else {
         tma_load_3d(smem + (to - base), &maps.v, bar, m0, sq.lo + t0, vh);
         bulk_load(to + L::B_P, rec + off_rest(true) + FRAG, FRAG, bar);
@@ -306,7 +307,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       }
       uint4 row4;
       {
-        const uint8_t* rows = smem + L::ROWS + (i & 1) * 2048;
+        const uint8_t* rows = smem + L::ROWS + (i & 1) * L::ROWB;
         row4 = *reinterpret_cast<const uint4*>(rows + kw * 512 + lane * 16);
         if (MODE == kFwd) {
           const uint32_t st = b0 + (i % SB) * L::B;
@@ -319,16 +320,14 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k) {
             const uint4 f = *reinterpret_cast<const uint4*>(sf + k * 512 + lane * 16);
-            const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+            const uint4 f2 = *reinterpret_cast<const uint4*>(sf + (DK / 16 + k) * 512 + lane * 16);
+            const uint32_t a[4] = {f.x, f.y, f.z, f.w}, a2[4] = {f2.x, f2.y, f2.z, f2.w};
             uint32_t b[4];
             ldmatrix4(b, st + box_at(16 * kw + ((mi >> 1) << 3) + ml, 2 * k + (mi & 1)));
-            if (k & 1) {
-              mma(z[0], a, b[0], b[1]);
-              mma(z[1], a, b[2], b[3]);
-            } else {
-              mma(y[0], a, b[0], b[1]);
-              mma(y[1], a, b[2], b[3]);
-            }
+            mma(y[0], a, b[0], b[1]);
+            mma(y[1], a, b[2], b[3]);
+            mma(z[0], a2, b[0], b[1]);
+            mma(z[1], a2, b[2], b[3]);
           }
           const float* vec = reinterpret_cast<const float*>(sp + L::B_VEC);
 #pragma unroll
@@ -337,25 +336,33 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[j][e] = (y[j][e] + z[j][e]) * (p.scale * ((e & 1) ? eg.y : eg.x));
           }
-          const uint32_t u[4] = {row4.x, row4.y, row4.z, row4.w};
+          const uint4 row2 = *reinterpret_cast<const uint4*>(rows + 2048 + kw * 512 + lane * 16);
+          const uint32_t u[4] = {row4.x, row4.y, row4.z, row4.w}, u2[4] = {row2.x, row2.y, row2.z, row2.w};
+          auto times = [&](float (&o)[2][4], const uint32_t (&a)[4], const uint32_t (&a2)[4], int jb) {
+            const uint8_t* pp = sp + L::B_P + block_of(kw, jb) * 512 + lane * 16;
+            const uint4 w = *reinterpret_cast<const uint4*>(pp), w2 = *reinterpret_cast<const uint4*>(pp + FRAG);
+            mma(o[0], a, w.x, w.y);
+            mma(o[1], a, w.z, w.w);
+            mma(o[0], a2, w.x, w.y);
+            mma(o[1], a2, w.z, w.w);
+            mma(o[0], a, w2.x, w2.y);
+            mma(o[1], a, w2.z, w2.w);
+          };
 #pragma unroll
           for (int jb = 0; jb < 3; ++jb) {
             if (jb >= kw) continue;
             const uint4 f = *reinterpret_cast<const uint4*>(rows + jb * 512 + lane * 16);
-            const uint4 w = *reinterpret_cast<const uint4*>(sp + L::B_P + block_of(kw, jb) * 512 + lane * 16);
-            const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-            mma(y[0], a, w.x, w.y);
-            mma(y[1], a, w.z, w.w);
+            const uint4 f2 = *reinterpret_cast<const uint4*>(rows + 2048 + jb * 512 + lane * 16);
+            const uint32_t a[4] = {f.x, f.y, f.z, f.w}, a2[4] = {f2.x, f2.y, f2.z, f2.w};
+            times(y, a, a2, jb);
           }
-          const uint4 w = *reinterpret_cast<const uint4*>(sp + L::B_P + block_of(kw, kw) * 512 + lane * 16);
           // a zero weight of a later token's row that is not finite would be NaN for
           // the tokens before it: then each token with the rows behind it left out
           float bad = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) bad = fmaf(0.f, low_half(u[e]), fmaf(0.f, high_half(u[e]), bad));
+          for (int e = 0; e < 4; ++e) bad = fmaf(0.f, low_half(u2[e]), fmaf(0.f, high_half(u2[e]), bad));   // (a high part stops at the largest number)
           if (!__any_sync(0xffffffffu, bad != 0.f)) {
-            mma(y[0], u, w.x, w.y);
-            mma(y[1], u, w.z, w.w);
+            times(y, u, u2, kw);
           } else {
             float o[2][4];
 #pragma unroll
@@ -365,16 +372,15 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
             }
 #pragma unroll 1
             for (int t = 0; t < 16; ++t) {
-              uint32_t a[4];
+              uint32_t a[4], a2[4];
+              rows_to(a, u, 0, t, tig);
+              rows_to(a2, u2, 0, t, tig);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int j = 8 * (e >> 1) + 2 * tig;
-                a[e] = u[e] & ((j <= t ? 0xffffu : 0u) | (j + 1 <= t ? 0xffff0000u : 0u));
                 o[0][e] = z[0][e];
                 o[1][e] = z[1][e];
               }
-              mma(o[0], a, w.x, w.y);
-              mma(o[1], a, w.z, w.w);
+              times(o, a, a2, kw);
 #pragma unroll
               for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -478,7 +484,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       split2(st[2 * ks + 1][2], st[2 * ks + 1][3], ah[3], al[3]);
       const int sf = L::SF + (i & 1) * L::SFB + (kw * KS + ks) * 512;
       *quad(sf) = make_uint4(ah[0], ah[1], ah[2], ah[3]);
-      if (MODE != kFwd) *quad(sf + (DK / 16) * 512) = make_uint4(al[0], al[1], al[2], al[3]);
+      *quad(sf + (DK / 16) * 512) = make_uint4(al[0], al[1], al[2], al[3]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         mma(x[2 * t], ah, b[t][0], b[t][1]);
@@ -625,7 +631,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       }
     }
     {
-      uint32_t uh[4], ul[4], w[4];
+      uint32_t uh[4], ul[4], w[4], w2[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = e >> 1, r = 2 * (e & 1);
@@ -635,12 +641,14 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
         } else {
           const float u0 = bt[j].x * ev[j][r], u1 = bt[j].y * ev[j][r + 1];
           split2(ec[j].x * u0, ec[j].y * u1, uh[e], ul[e]);
-          w[e] = MODE == kFwd ? pack2(u0, u1) : pack2(ev[j][r], ev[j][r + 1]);
+          if (MODE == kFwd) split2(u0, u1, w[e], w2[e]);
+          else w[e] = pack2(ev[j][r], ev[j][r + 1]);
         }
       }
       *quad(L::FU + kw * 1024) = make_uint4(uh[0], uh[1], uh[2], uh[3]);
       if (LO) *quad(L::FU + kw * 1024 + 512) = make_uint4(ul[0], ul[1], ul[2], ul[3]);
-      *quad(L::ROWS + (i & 1) * 2048 + kw * 512) = make_uint4(w[0], w[1], w[2], w[3]);
+      *quad(L::ROWS + (i & 1) * L::ROWB + kw * 512) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (MODE == kFwd) *quad(L::ROWS + (i & 1) * L::ROWB + 2048 + kw * 512) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
     }
     // 4. this warp's quarter of the state
     uint32_t kt[4][KS][4], qt[MODE == kRev ? 4 : 1][KS][4];
@@ -700,11 +708,11 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
 }
 
 // ORDER: packed sequences (where it is not wanted its registers cost 1 % of the time)
-template <int DK, bool LO, bool ORDER>
+template <int DK, bool ORDER>
 __global__ void __launch_bounds__(2 * NH, 1)
 gated_split_kernel(const SplitArgs p, const __grid_constant__ SplitMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  split_chain<DK, kFwd, LO, ORDER>(p, maps, blockIdx.x, smem);
+  split_chain<DK, kFwd, true, ORDER>(p, maps, blockIdx.x, smem);
 }
 
 // Both chains of the backward in one launch (order: second_chain).
@@ -742,7 +750,7 @@ cudaError_t launch(SplitArgs f, int B, const SplitArgs* save, cudaStream_t strea
   f.nblk = f.dv / 16;
   const long long grid = (long long)f.nseq * f.H * f.nblk * (save != nullptr ? 2 : 1);
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  constexpr int kF = SplitSmem<DK, kFwd, LO>::TOTAL, kR = SplitSmem<DK, kRev, LO>::TOTAL, kS = SplitSmem<DK, kSave, false>::TOTAL;
+  constexpr int kF = SplitSmem<DK, kFwd, true>::TOTAL, kR = SplitSmem<DK, kRev, LO>::TOTAL, kS = SplitSmem<DK, kSave, false>::TOTAL;
   cudaError_t e;
   SplitMaps fm, bm;
   if (!make_maps(&fm, f, B, DK) || (save != nullptr && !make_maps(&bm, *save, B, DK))) return cudaErrorInvalidValue;
@@ -750,7 +758,7 @@ cudaError_t launch(SplitArgs f, int B, const SplitArgs* save, cudaStream_t strea
   if (f.status == nullptr) return cudaErrorNotReady;
   f.stall = take_gated_timeout_test(0) ? 1 : 0;
   if (save == nullptr) {
-    auto kern = f.offsets != nullptr ? gated_split_kernel<DK, LO, true> : gated_split_kernel<DK, LO, false>;
+    auto kern = f.offsets != nullptr ? gated_split_kernel<DK, true> : gated_split_kernel<DK, false>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kF);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, 2 * NH, kF, stream>>>(f, fm);
@@ -771,7 +779,7 @@ cudaError_t launch(SplitArgs f, int B, const SplitArgs* save, cudaStream_t strea
 }
 
 cudaError_t dispatch(const SplitArgs& f, const SplitArgs* save, int B, int dk, cudaStream_t stream) {
-  const bool lo = f.S_out != nullptr;
+  const bool lo = save == nullptr || f.S_out != nullptr;
   if (dk == 64) return lo ? launch<64, true>(f, B, save, stream) : launch<64, false>(f, B, save, stream);
   return lo ? launch<128, true>(f, B, save, stream) : launch<128, false>(f, B, save, stream);
 }

@@ -531,11 +531,10 @@ LA_API la_status la_state_unpack(const unsigned char* codes, const unsigned char
  * up to 2^31 - 1. Nothing is joined by atomics: results repeat bit for bit.
  *
  * Where la_gated_delta_path is 1 (bf16, dk and dv in {64, 128}) whole sequences
- * are computed in chunks of 64 tokens on the tensor cores. Where a state is asked for (S_final, dS0),
- * fp32 operands of a product that reaches it go in as bf16 high and low parts (states within
- * 1e-5 of their 2-norm on unit-norm keys); otherwise every operand is rounded to bf16
- * once, so that the rows of a call without a state may differ from one with it in their last
- * bits. Otherwise, for N <= 32, and backward for up to 1024 rows of all heads and batch entries
+ * are computed in chunks of 64 tokens on the tensor cores; fp32 operands of a
+ * product go in as bf16 high and low parts (states within 1e-5 of their 2-norm on unit-norm
+ * keys in random directions, within 3e-5 on keys that are nearly equal; outputs as those of fp32
+ * arithmetic). Otherwise, for N <= 32, and backward for up to 1024 rows of all heads and batch entries
  * (N <= 256), token by token in fp32. The tensor core kernels' waits are bounded:
  * la_device_status has LA_ERR_TIMEOUT if one ever ran out.
  */
