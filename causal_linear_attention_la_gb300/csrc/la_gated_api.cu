@@ -78,16 +78,6 @@ bool use_mma(int N, int dk, int dv, la_dtype dtype) {
   return N > kShortN && current_path() == LA_PATH_AUTO && gated_on_tensor_cores(dk, dv, dtype);
 }
 
-// Backward, a token's dg is what is left of sums that partly cancel, to which
-// operands rounded to bf16 leave 3.3e-3 of dg's 2-norm on the average, but 4e-3 to 1e-2 where one
-// or two chunks make up that norm. Few tokens of few heads (a gradient check) are taken in
-// fp32: 1.7e-3, the rounding of dg itself, in 97 us at 16 heads of 64 tokens against 33.
-// Long sequences of few heads are not, whose time that would multiply.
-constexpr int kFewTokens = 1024, kFewN = 256;
-bool use_mma_backward(int B, int H, int N, int dk, int dv, la_dtype dtype) {
-  return use_mma(N, dk, dv, dtype) && (N > kFewN || (long long)B * H * N > kFewTokens);
-}
-
 bool packed_size(int B, int nseq) { return B == 1 && nseq != 1; }
 
 // Strides of rows [B][N][heads][d]; where they are written, no two rows may
@@ -207,7 +197,7 @@ la_status la_forward_gated_delta(const void* q, const void* k, const void* v, co
 size_t la_backward_gated_delta_workspace_size(int B, int Hk, int H, int N, int dk, int dv, int nseq, la_dtype dtype) {
   bool empty = false;
   if (check_sizes("", B, Hk, H, N, dk, dv, nseq, 1.f, dtype, packed_size(B, nseq), &empty) != LA_OK || empty) return 0;
-  return use_mma_backward(B, H, N, dk, dv, dtype) ? mma_gated_backward_workspace(B, H, N, dk, dv, nseq, B == 1)
+  return use_mma(N, dk, dv, dtype) ? mma_gated_backward_workspace(B, H, N, dk, dv, nseq, B == 1)
                                                   : simt_gated_backward_workspace(B, H, N, dk, dv, nseq, B == 1);
 }
 
@@ -229,7 +219,7 @@ la_status la_backward_gated_delta(const void* q, const void* k, const void* v, c
   const size_t need = la_backward_gated_delta_workspace_size(B, Hk, H, N, dk, dv, nseq, dtype);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(LA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, got %zu", who, need, workspace_bytes);
-  const cudaError_t e = use_mma_backward(B, H, N, dk, dv, dtype) ? mma_gated_backward(a) : simt_gated_backward(a);
+  const cudaError_t e = use_mma(N, dk, dv, dtype) ? mma_gated_backward(a) : simt_gated_backward(a);
   return e == cudaSuccess ? LA_OK : cuda_fail(e, who);
 }
 

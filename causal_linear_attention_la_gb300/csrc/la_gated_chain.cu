@@ -29,18 +29,18 @@ using sm100::tma_load_3d;
 
 enum { kFwd = 0, kSave = 1, kRev = 2 };
 // W: warps of a CTA
-template <int DK, int MODE, bool LO, int W>
+template <int DK, int MODE, int W>
 struct ChainSmem {
   static constexpr int KB = C * DK * 2;             // a tile of K or Q
   static constexpr int VB = C * W * 32;             // the CTA's columns of V or dO
-  // the part of the record that is wanted: all, [T hi | vec],
+  // the part of the record that is wanted: all, [T lo | T hi | vec],
   // [vec | T^T hi | P^T hi | T^T lo | P^T lo]
-  static constexpr int FROM = MODE == kRev ? off_vec(true) : 0;
-  static constexpr int RB = MODE == kFwd ? REC_FWD : MODE == kSave ? off_rest(true) : VEC + (LO ? 4 : 2) * FRAG;
-  static constexpr int RV = MODE == kRev ? 0 : off_vec(MODE != kFwd);          // vec in it
+  static constexpr int FROM = MODE == kRev ? OFF_VEC : 0;
+  static constexpr int RB = (MODE == kFwd ? REC_FWD : MODE == kSave ? OFF_REST : OFF_SUMS) - FROM;
+  static constexpr int RV = OFF_VEC - FROM;          // vec in it
   __host__ __device__ static constexpr int tri(int i) {   // T hi, T lo, P hi, P lo (reverse: T^T, P^T)
     return MODE == kRev ? VEC + (i == 1 ? 2 : i == 2 ? 1 : i) * FRAG
-                        : i == 0 ? (MODE == kFwd ? FRAG : 0) : i == 1 ? 0 : RV + VEC + (i - 2) * FRAG;
+                        : i == 0 ? FRAG : i == 1 ? 0 : RV + VEC + (i - 2) * FRAG;
   }
   static constexpr int K = 0;
   static constexpr int Q = K + KB;
@@ -59,8 +59,9 @@ struct ChainArgs {
   const float* S_in; float* S_out;
   const int* offsets;
   __nv_bfloat16* out;                    // O, E or dR rows [B,H,N,dv]
+  __nv_bfloat16* out_lo;                 // E, dR: what that leaves out
   __nv_bfloat16* states;                 // [slot,H,dv,DK]: before each chunk (save), behind it (reverse)
-  __nv_bfloat16* states_lo;              // what that leaves out, or null
+  __nv_bfloat16* states_lo;              // what that leaves out
   int Hk, H, N, dv, nseq, nblk;
   float scale;
   int* status;
@@ -70,9 +71,9 @@ struct ChainArgs {
 // Maps of [heads][rows][DK], of [heads][rows][dv], in boxes of 64 columns and 64 rows
 struct ChainMaps { CUtensorMap q, k, v; };
 
-template <int DK, int MODE, bool LO, int W>
+template <int DK, int MODE, int W>
 __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps, long long block, uint8_t* smem) {
-  using L = ChainSmem<DK, MODE, LO, W>;
+  using L = ChainSmem<DK, MODE, W>;
   constexpr int NT = 32 * W, KS = DK / 16;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, ml = lane & 7;
@@ -85,6 +86,7 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
   const long long vrow = (long long)vh * p.N + sq.lo;
   const int m0 = blk * 16 * W + warp * 16;           // this warp's first column
   __nv_bfloat16* ob = p.out + vrow * p.dv + m0;
+  __nv_bfloat16* ol = MODE == kFwd ? nullptr : p.out_lo + vrow * p.dv + m0;
   const uint32_t base = smem_addr(smem);
   uint8_t* rows = smem + L::OUT + warp * C * 32;
   const uint32_t rows_at = base + L::OUT + warp * C * 32;
@@ -123,6 +125,31 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
       for (int e = 0; e < 4; ++e)
         st[j][e] = src == nullptr ? 0.f : src[(long long)(8 * j + 2 * tig + (e & 1)) * p.dv + 8 * (e >> 1)];
   }
+
+  // rows [token][16 columns] by way of this warp's part of shared memory, 16 bytes a lane:
+  // rounded, and (backward) what that leaves out
+  auto rows_out = [&](const float (&x)[8][4], int t0, int cn) {
+#pragma unroll
+    for (int part = 0; part < (MODE == kFwd ? 1 : 2); ++part) {
+      __nv_bfloat16* to = part == 0 ? ob : ol;
+      __syncwarp();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        uint32_t w[2][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2_out(x[2 * t + (e >> 1)][2 * (e & 1)], x[2 * t + (e >> 1)][2 * (e & 1) + 1], w[0][e], w[1][e]);
+        stmatrix4t(rows_at + tile_at<2>(16 * t + ((mi >> 1) << 3) + ml, mi & 1), w[part][0], w[part][1], w[part][2], w[part][3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * r + (lane >> 1), half = lane & 1;
+        if (t < cn)
+          *reinterpret_cast<uint4*>(to + (long long)(t0 + t) * p.dv + 8 * half) =
+              *reinterpret_cast<const uint4*>(rows + tile_at<2>(t, half));
+      }
+    }
+  };
 
   for (int i = 0; i < nchunks; ++i) {
     const int c = chunk_of(i), t0 = c * C, cn = min(C, n - t0);
@@ -193,7 +220,7 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           join(p.states, 2 * ks, r, ah[r], ah[2 + r]);
-          if (p.states_lo != nullptr) join(p.states_lo, 2 * ks, r, al[r], al[2 + r]);
+          join(p.states_lo, 2 * ks, r, al[r], al[2 + r]);
         }
       }
 #pragma unroll
@@ -201,12 +228,10 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
         mma(x[2 * t], ah, b[t][0], b[t][1]);
         mma(x[2 * t + 1], ah, b[t][2], b[t][3]);
       }
-      if (LO) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          mma(x[2 * t], al, b[t][0], b[t][1]);
-          mma(x[2 * t + 1], al, b[t][2], b[t][3]);
-        }
+      for (int t = 0; t < 4; ++t) {
+        mma(x[2 * t], al, b[t][0], b[t][1]);
+        mma(x[2 * t + 1], al, b[t][2], b[t][3]);
       }
       if (MODE == kFwd) {
 #pragma unroll
@@ -250,7 +275,6 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
           const uint4 th = frag(0, block_of(tb, jb));
           mma(ev[2 * tb], rh[jb], th.x, th.y);
           mma(ev[2 * tb + 1], rh[jb], th.z, th.w);
-          if (!LO) continue;
           const uint4 tl = frag(1, block_of(tb, jb));
           mma(ev[2 * tb], rl[jb], th.x, th.y);
           mma(ev[2 * tb + 1], rl[jb], th.z, th.w);
@@ -307,7 +331,6 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
               }
               const uint4 th = frag(0, block_of(tb, jb));
               mma(e2[0], a, th.x, th.y); mma(e2[1], a, th.z, th.w);
-              if (!LO) continue;
               const uint4 tl = frag(1, block_of(tb, jb));
               mma(e2[0], b, th.x, th.y); mma(e2[1], b, th.z, th.w);
               mma(e2[0], a, tl.x, tl.y); mma(e2[1], a, tl.z, tl.w);
@@ -378,14 +401,7 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
           }
         }
       }
-      // rows [token][16 columns] over this warp's part of V, then 16 bytes a lane
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float (&a)[4] = MODE == kFwd ? y[2 * t] : ev[2 * t];
-        const float (&b)[4] = MODE == kFwd ? y[2 * t + 1] : ev[2 * t + 1];
-        stmatrix4t(rows_at + tile_at<2>(16 * t + ((mi >> 1) << 3) + ml, mi & 1), pack2(a[0], a[1]),
-                   pack2(a[2], a[3]), pack2(b[0], b[1]), pack2(b[2], b[3]));
-      }
+      if constexpr (MODE == kFwd) rows_out(y, t0, cn); else rows_out(ev, t0, cn);
       // 5. S^T
       uint32_t kt[2][KS][4];
       auto ask_t = [&](int t) {
@@ -414,12 +430,10 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
           mma(st[2 * k2], uh, kt[t & 1][k2][0], kt[t & 1][k2][1]);
           mma(st[2 * k2 + 1], uh, kt[t & 1][k2][2], kt[t & 1][k2][3]);
         }
-        if (LO) {
 #pragma unroll
-          for (int k2 = 0; k2 < KS; ++k2) {
-            mma(st[2 * k2], ul, kt[t & 1][k2][0], kt[t & 1][k2][1]);
-            mma(st[2 * k2 + 1], ul, kt[t & 1][k2][2], kt[t & 1][k2][3]);
-          }
+        for (int k2 = 0; k2 < KS; ++k2) {
+          mma(st[2 * k2], ul, kt[t & 1][k2][0], kt[t & 1][k2][1]);
+          mma(st[2 * k2 + 1], ul, kt[t & 1][k2][2], kt[t & 1][k2][3]);
         }
       }
     } else {
@@ -444,7 +458,6 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
           const uint4 ph = frag(2, block_of(tb, jb));
           mma(x[2 * jb], dof[tb], ph.x, ph.y);
           mma(x[2 * jb + 1], dof[tb], ph.z, ph.w);
-          if (!LO) continue;
           const uint4 pl = frag(3, block_of(tb, jb));
           mma(x[2 * jb], dof[tb], pl.x, pl.y);
           mma(x[2 * jb + 1], dof[tb], pl.z, pl.w);
@@ -470,18 +483,13 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
           const uint4 th = frag(0, block_of(tb, jb));
           mma(y[2 * jb], rh[tb], th.x, th.y);
           mma(y[2 * jb + 1], rh[tb], th.z, th.w);
-          if (!LO) continue;
           const uint4 tl = frag(1, block_of(tb, jb));
           mma(y[2 * jb], rl[tb], th.x, th.y);
           mma(y[2 * jb + 1], rl[tb], th.z, th.w);
           mma(y[2 * jb], rh[tb], tl.x, tl.y);
           mma(y[2 * jb + 1], rh[tb], tl.z, tl.w);
         }
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        stmatrix4t(rows_at + tile_at<2>(16 * t + ((mi >> 1) << 3) + ml, mi & 1),
-                   pack2(y[2 * t][0], y[2 * t][1]), pack2(y[2 * t][2], y[2 * t][3]),
-                   pack2(y[2 * t + 1][0], y[2 * t + 1][1]), pack2(y[2 * t + 1][2], y[2 * t + 1][3]));
+      rows_out(y, t0, cn);
       // dS^T = e^{G_C} dS^T + (scale e^G dO)^T Q - (e^G dR)^T K
 #pragma unroll
       for (int j = 0; j < 2 * KS; ++j)
@@ -507,7 +515,7 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
             ldmatrix4t(d[x], sb + L::K + at);
           }
 #pragma unroll
-          for (int part = 0; part < (LO ? 4 : 2); ++part)
+          for (int part = 0; part < 4; ++part)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const uint32_t (&w)[4] = part & 1 ? d[x] : b[x];
@@ -516,15 +524,6 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
               mma(st[2 * (k4 + x) + 1], f, w[2], w[3]);
             }
         }
-      }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * r + (lane >> 1), half = lane & 1;
-      if (t < cn) {
-        const uint4 w = *reinterpret_cast<const uint4*>(rows + tile_at<2>(t, half));
-        *reinterpret_cast<uint4*>(ob + (long long)(t0 + t) * p.dv + 8 * half) = w;
       }
     }
   }
@@ -541,23 +540,22 @@ template <int DK, int W>
 __global__ void __launch_bounds__(32 * W)
 gated_chain_kernel(const ChainArgs p, const __grid_constant__ ChainMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  chain<DK, kFwd, true, W>(p, maps, blockIdx.x, smem);
+  chain<DK, kFwd, W>(p, maps, blockIdx.x, smem);
 }
 
 // Both chains of the backward in one launch (they need nothing of each other; order:
-// second_chain). The states before the chunks are kept as bf16 whatever is
-// asked for: that chain takes operands rounded once.
-template <int DK, bool LO, int W>
+// second_chain).
+template <int DK, int W>
 __global__ void __launch_bounds__(32 * W)
 gated_chains_kernel(const ChainArgs rev, const __grid_constant__ ChainMaps rmaps, const ChainArgs save,
                     const __grid_constant__ ChainMaps smaps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   unsigned number;
-  if (second_chain(blockIdx.x, gridDim.x, rev.offsets != nullptr, rev.nblk * rev.H, number)) chain<DK, kSave, false, W>(save, smaps, number, smem);
-  else chain<DK, kRev, LO, W>(rev, rmaps, number, smem);
+  if (second_chain(blockIdx.x, gridDim.x, rev.offsets != nullptr, rev.nblk * rev.H, number)) chain<DK, kSave, W>(save, smaps, number, smem);
+  else chain<DK, kRev, W>(rev, rmaps, number, smem);
 }
 
-template <int DK, bool LO, int W>
+template <int DK, int W>
 cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
   f.nblk = a.dv / (16 * W);
   const long long grid = (long long)f.nseq * f.H * f.nblk * (save != nullptr ? 2 : 1);
@@ -572,7 +570,7 @@ cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
   cudaError_t e;
   if (save == nullptr) {
     auto kern = gated_chain_kernel<DK, W>;
-    const int smem = ChainSmem<DK, kFwd, true, W>::TOTAL;
+    const int smem = ChainSmem<DK, kFwd, W>::TOTAL;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, 32 * W, smem, a.stream>>>(f, m);
@@ -583,9 +581,9 @@ cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
     b.stall = f.stall;
     ms = m;
     if (!gated_map(&ms.v, b.v, heads, a.N, a.dv, 64)) return cudaErrorInvalidValue;
-    auto kern = gated_chains_kernel<DK, LO, W>;
-    constexpr int smem = ChainSmem<DK, kRev, LO, W>::TOTAL;
-    static_assert(smem >= ChainSmem<DK, kSave, false, W>::TOTAL, "the reverse chain has more");
+    auto kern = gated_chains_kernel<DK, W>;
+    constexpr int smem = ChainSmem<DK, kRev, W>::TOTAL;
+    static_assert(smem >= ChainSmem<DK, kSave, W>::TOTAL, "the reverse chain has more");
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, 32 * W, smem, a.stream>>>(f, m, b, ms);
@@ -596,10 +594,8 @@ cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
 }
 
 cudaError_t dispatch(const GatedArgs& a, const ChainArgs& f, const ChainArgs* save) {
-  const bool lo = save == nullptr || f.S_out != nullptr;
-  if (save == nullptr && a.dv == 128) return a.dk == 64 ? launch<64, true, 8>(a, f, save) : launch<128, true, 8>(a, f, save);
-  if (a.dk == 64) return lo ? launch<64, true, 4>(a, f, save) : launch<64, false, 4>(a, f, save);
-  return lo ? launch<128, true, 4>(a, f, save) : launch<128, false, 4>(a, f, save);
+  if (a.dv == 128) return a.dk == 64 ? launch<64, 8>(a, f, save) : launch<128, 8>(a, f, save);
+  return a.dk == 64 ? launch<64, 4>(a, f, save) : launch<128, 4>(a, f, save);
 }
 
 ChainArgs chain_args(const GatedArgs& a, const uint8_t* rec, int rec_bytes) {
@@ -617,11 +613,11 @@ cudaError_t gated_chain_forward(const GatedArgs& a, const uint8_t* records) {
   return dispatch(a, p, nullptr);
 }
 
-cudaError_t gated_chain_backward(const GatedArgs& a, const uint8_t* records, __nv_bfloat16* e,
-                                 __nv_bfloat16* const (&states)[4]) {
+cudaError_t gated_chain_backward(const GatedArgs& a, const uint8_t* records, const ChainOut& o) {
   ChainArgs r = chain_args(a, records, REC_BWD), s = r;
-  r.v = a.dout; r.S_in = a.dS; r.S_out = a.dS0; r.out = (__nv_bfloat16*)a.dv_; r.states = states[1]; r.states_lo = states[3];
-  s.S_in = a.S0; s.out = e; s.states = states[0]; s.states_lo = states[2];
+  r.v = a.dout; r.S_in = a.dS; r.S_out = a.dS0; r.out = (__nv_bfloat16*)a.dv_; r.out_lo = o.dr_lo;
+  r.states = o.dstates; r.states_lo = o.dstates_lo;
+  s.S_in = a.S0; s.out = o.e; s.out_lo = o.e_lo; s.states = o.states; s.states_lo = o.states_lo;
   return dispatch(a, r, &s);
 }
 

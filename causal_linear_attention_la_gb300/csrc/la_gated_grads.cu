@@ -2,33 +2,30 @@
 // the tensor cores (tcgen05), from the states before each chunk (S_0), their gradients
 // behind it (dS), E and dR as the chains left them (formulas: la_gated_simt.cu,
 // notation: la_gated_mma.cuh):
-//   N_tj = -D_tj (dR_t.E_j) beta_j (j < t),   W_tj = scale D_tj (dO_t.E_j) beta_j (j <= t),
-//   dK = -e^G (dR S_0^T) + e^{G_C-G} beta (E dS^T) + N K + N^T K + W^T Q
-//   dQ = scale e^G (dO S_0^T) + W K
+//   N_tj = -D_tj (dR_t.E_j) (j < t),   W_tj = scale D_tj (dO_t.E_j) (j <= t),
+//   dK = -e^G (dR S_0^T) + beta (e^{G_C-G} E dS^T + N^T K + W^T Q) + (N beta) K
+//   dQ = scale e^G (dO S_0^T) + (W beta) K
 // Every sum that dbeta and dg want is a product of a row with k or q:
-//   dbeta_t = k_t.(e^{G_C-G} E dS^T)_t + k_t.(N^T K + W^T Q)_t / beta_t
-//   dG_t = q_t.dQ_t + k_t.(-e^G dR S_0^T + N K)_t - beta_t dbeta_t,
+//   dbeta_t = k_t.(e^{G_C-G} E dS^T + N^T K + W^T Q)_t
+//   dG_t = q_t.dQ_t + k_t.(-e^G dR S_0^T + (N beta) K)_t - beta_t dbeta_t,
 // plus, at the chunk's end, sum_t beta_t k_t.(e^{G_C-G} E dS^T)_t + e^{G_C} S_0.dS; dg
 // is the sum from each token to the end. A pair (t, j) adds what it takes away in that
-// sum, once from row t and once from column j: both come from the same bf16 values of N and W, so that
-// it leaves nothing. (Rounded apart, the pairs' differences were 9e-3 of dg.) Where
-// |beta_j| < 2^-30 column j has 2^-30 in its place in N^T and W^T, whose row j
-// then counts beta_j 2^30 times (a power of two near the others' sizes: with 2^-100 gradients
-// of 1e-9 fell below bf16's normal numbers).
+// sum, once from row t and once from column j, and where keys are alike the others cancel
+// too: S_0, dS, E, dR, N, W and N beta, W beta are bf16 high and low parts, a product's lo lo left
+// out (rounded once each, dg was off by 3e-3 of its two-norm with independent keys, by up to
+// 1.5e-1 with cosines of 0.9 between them).
 // Products (M = 128, A and B in shared memory with the 128-byte swizzle, fp32 in
 // tensor memory; a lane is a token's row: lanes 0-63 of dK, 64-127 of dQ):
-//   1. [dR; dO] E^T                 [128 x 64]
-//   2. [E; dR] dS^T, [dR; dO] S_0^T [128 x DK]   (lanes 64-127 of the first unused)
-//   3. [N; W] K, [N^T W^T] [K; Q]   [128 x DK]   (lanes 64-127 of the second unused)
-// 2048 cycles of the tensor pipe at d = 128. Operands are bf16 (one rounding each of S_0, dS,
-// E, dR, N and W); sums are fp32.
+//   1. [dR; dO] E^T                 [128 x 64], the low part of dR in columns of its own,
+//   2. [dR; dO] S_0^T, [E; .] dS^T  [128 x DK]  since dO has none
+//   3. [N; W] beta K, [N; W]^T [K; Q]
+// (lanes 64-127 of what sums dR's low part, E dS^T and the transposed product are unused).
 //
-// Bound: HBM (150 KB a chunk and head at d = 128, the two states 64 of them). One
-// CTA of 16 warps per SM goes through the chunks; a key head's heads of values follow
-// each other, so that dQ and dK of shared heads are summed in registers, in a
-// fixed order. The next head's rows are on their way from the start of a head on, its
-// states from the end of step 2. (The same products by mma.sync took 282 us for 64
-// heads of 4096 tokens: fragments through the shared-memory pipe and barriers.)
+// Bound: HBM (272 KB a chunk and head at d = 128, the two states 128 of them) and the
+// way from load to product to product of one CTA of 16 warps per SM, which goes through the
+// chunks; a key head's heads of values follow each other, so that dQ and dK of shared heads
+// are summed in registers, in a fixed order. The states come in pieces of 64 values, the
+// next head's while N and W are multiplied; its rows take the place of N and W.
 #include "la_gated_mma.cuh"
 
 namespace la {
@@ -40,7 +37,6 @@ using namespace sm100;
 
 constexpr int NT = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;       // bound of every wait for the tensor cores
-constexpr float kTiny = 9.313225746154785e-10f, kHuge = 1073741824.f;   // 2^-30, 2^30
 
 // 32 lanes x 16 consecutive 32-bit columns of tensor memory.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -54,30 +50,34 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 
 template <int DK, int DV>
 struct GradSmem {
-  static constexpr int KBOX = 128 * 128, RBOX = 192 * 128, SBOX = DV * 128;   // boxes of 64 columns
+  // Boxes of 64 columns. Rows [E hi; E lo; dR lo; dR hi; dO]: what product takes as its 128
+  // rows starts at any of them.
+  static constexpr int KBOX = 128 * 128, RBOX = 320 * 128;
   static constexpr int KQB = (DK / 64) * KBOX;       // [K; Q]
-  static constexpr int ROWB = (DV / 64) * RBOX;      // [E; dR; dO]
-  static constexpr int SB = (DK / 64) * SBOX;        // a state, rows dv
-  static constexpr int KQ = 0;                       // two units'
-  static constexpr int ROWS = KQ + 2 * KQB;          // two heads'
-  static constexpr int S0 = ROWS + 2 * ROWB;
-  static constexpr int DS = S0 + SB;
-  // [N; W] 16 KB, [N^T W^T] 16 KB (the product reads the 8 KB behind it as rows that
-  // nobody uses), then the rows' sums: over a head's rows after step 2 where they fit
-  static constexpr int WSIZE = 32768 + 8192;
-  static constexpr bool kOver = ROWB >= WSIZE;
-  static constexpr int WEXTRA = DS + SB;
-  static constexpr int VECS = WEXTRA + (kOver ? 0 : WSIZE);   // two heads' e^G, e^{G_C-G}, beta, G high and low
-  static constexpr int CTRL = VECS + 2 * 5 * C * 4;           // barriers, tensor memory's address, flags, 16 sums
+  static constexpr int ROWB = (DV / 64) * RBOX;
+  static constexpr int kEh = 0, kEl = 64 * 128, kRl = 128 * 128, kRh = 192 * 128;
+  // a piece of a state: 64 values of its high and of its low part, rows dv
+  static constexpr int PART = (DK / 64) * 8192, PIECE = 2 * PART;
+  static constexpr int NP = 2 * (DV / 64);           // pieces a head: S_0, dS, S_0, dS
+  // over a head's rows after step 2: [N; W] high and low, [N; W] beta high and low, the rows' sums
+  static constexpr int TILE = 16384, SUMS = 4 * TILE, WSIZE = SUMS + 4096;
+  static constexpr int KQ = 0;
+  static constexpr int ROWS = KQ + KQB;
+  static constexpr int PIECES = ROWS + (ROWB > WSIZE ? ROWB : WSIZE);
+  static constexpr int REST = 5 * C * 4 + 128;       // e^G, e^{G_C-G}, beta, G high and low; control
+  static constexpr int SLOTS = PIECES + NP * PIECE + REST <= 227 * 1024 ? NP : 3;
+  static constexpr int VECS = PIECES + SLOTS * PIECE;
+  static constexpr int CTRL = VECS + 5 * C * 4;      // barriers, tensor memory's address, a flag, 16 sums
   static constexpr int TOTAL = CTRL + 128;
-  static constexpr int D1 = 0, D2 = 128, D5A = 256, D5B = 384, D3 = 384;      // columns of tensor memory
+  // columns of tensor memory: dR hi and dO, dR lo times S_0; E dS^T; the same two times E; step 3
+  static constexpr int D1 = 0, D1B = 128, D2 = 256, D3 = 384, D3B = 448, D5A = 384, D5B = 128;
   static_assert(TOTAL <= 227 * 1024, "shared memory");
+  static_assert(SLOTS == NP || NP == 4, "the fourth piece takes the first one's place");
 };
 
 struct GradArgs {
-  const __nv_bfloat16* q; const __nv_bfloat16* k; const __nv_bfloat16* dout; const __nv_bfloat16* e;
-  const __nv_bfloat16* dr; const __nv_bfloat16* states; const __nv_bfloat16* dstates;
-  const __nv_bfloat16* states_lo; const __nv_bfloat16* dstates_lo;     // or null
+  const __nv_bfloat16* q; const __nv_bfloat16* k; const __nv_bfloat16* dout; const __nv_bfloat16* dr;
+  ChainOut c;
   const uint8_t* rec;
   const int4* chunks;                                // of every slot: its batch entry, first row, number of tokens
   __nv_bfloat16* dq; __nv_bfloat16* dk; __nv_bfloat16* dg; __nv_bfloat16* dbeta;
@@ -114,12 +114,13 @@ gated_grads_tc_kernel(const GradArgs p) {
   using L = GradSmem<DK, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int KCH = DK / 8, VCH = DV / 8, HC = DK / 4;     // HC: columns of a warp's quarter
+  constexpr int FIRST = L::SLOTS < L::NP ? L::SLOTS : L::NP;  // pieces asked for ahead
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = smem_addr(smem);
   const int group = p.H / p.Hk;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::CTRL);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::CTRL + 32);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::CTRL + 40);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::CTRL + 40);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::CTRL + 44);
   float* dots = reinterpret_cast<float*>(smem + L::CTRL + 64);
 
   auto unit_at = [&](unsigned u) {                   // the next unit with tokens from u on
@@ -135,47 +136,51 @@ gated_grads_tc_kernel(const GradArgs p) {
     }
     return x;
   };
-  auto load_rows = [&](const Unit& x, int hh, int buf, int kbuf) {
+  auto load_rows = [&](const Unit& x, int hh) {
     if (hh == 0) {
       const long long r = (((long long)x.b * p.Hk + x.hk) * p.N + x.row) * DK;
-      const uint32_t to = base + L::KQ + kbuf * L::KQB;
-      load_box<KCH>(to, 0, L::KBOX, p.k + r, x.n, tid);
-      load_box<KCH>(to, 64, L::KBOX, p.q + r, x.n, tid);
+      load_box<KCH>(base + L::KQ, 0, L::KBOX, p.k + r, x.n, tid);
+      load_box<KCH>(base + L::KQ, 64, L::KBOX, p.q + r, x.n, tid);
     }
     const int h = x.hk * group + hh;
     const long long r = (((long long)x.b * p.H + h) * p.N + x.row) * DV;
-    const uint32_t to = base + L::ROWS + buf * L::ROWB;
-    load_box<VCH>(to, 0, L::RBOX, p.e + r, x.n, tid);
-    load_box<VCH>(to, 64, L::RBOX, p.dr + r, x.n, tid);
-    load_box<VCH>(to, 128, L::RBOX, p.dout + r, x.n, tid);
+    const __nv_bfloat16* const src[5] = {p.c.e, p.c.e_lo, p.c.dr_lo, p.dr, p.dout};
+#pragma unroll
+    for (int i = 0; i < 5; ++i) load_box<VCH>(base + L::ROWS, 64 * i, L::RBOX, src[i] + r, x.n, tid);
     const uint8_t* rec = p.rec + ((long long)x.slot * p.H + h) * REC_BWD;
-    load_bytes<VEC, NT>(base + L::VECS + buf * 5 * C * 4, rec + off_vec(true), tid);
-    load_bytes<2 * C * 4, NT>(base + L::VECS + buf * 5 * C * 4 + VEC, rec + OFF_SUMS, tid);
+    load_bytes<VEC, NT>(base + L::VECS, rec + OFF_VEC, tid);
+    load_bytes<2 * C * 4, NT>(base + L::VECS + VEC, rec + OFF_SUMS, tid);
     cp_commit();
   };
-  auto load_states = [&](const Unit& x, int hh) {
-    const long long at = ((long long)x.slot * p.H + x.hk * group + hh) * DK * DV;
+  // piece j of a head (S_0 or dS, values 64 (j / 2) ..), in slot (turn + j) % SLOTS
+  auto at_piece = [&](unsigned turn, int j) { return L::PIECES + (int)((turn + j) % L::SLOTS) * L::PIECE; };
+  auto load_piece = [&](const Unit& x, int hh, unsigned turn, int j) {
+    const long long at = (((long long)x.slot * p.H + x.hk * group + hh) * DV + 64 * (j >> 1)) * DK;
+    const __nv_bfloat16* hi = ((j & 1) ? p.c.dstates : p.c.states) + at;
+    const __nv_bfloat16* lo = ((j & 1) ? p.c.dstates_lo : p.c.states_lo) + at;
+    const uint32_t to = base + at_piece(turn, j);
 #pragma unroll
-    for (int i = 0; i < DV * KCH / NT; ++i) {
-      const int j = tid + i * NT;
-      cp16(base + L::DS + box_at(j / KCH, j % KCH, L::SBOX), p.dstates + at + j * 8, true);
-      cp16(base + L::S0 + box_at(j / KCH, j % KCH, L::SBOX), p.states + at + j * 8, true);
+    for (int i = 0; i < 64 * KCH / NT; ++i) {
+      const int e = tid + i * NT;
+      const uint32_t off = box_at(e / KCH, e % KCH, 8192);
+      cp16(to + off, hi + e * 8, true);
+      cp16(to + L::PART + off, lo + e * 8, true);
     }
     cp_commit();
   };
 
   Unit x = unit_at(blockIdx.x);
   if (x.u >= p.units) return;
-  int hh = 0, buf = 0, kbuf = 0;
-  load_rows(x, 0, 0, 0);
-  load_states(x, 0);
+  int hh = 0;
+  load_rows(x, 0);
+  for (int j = 0; j < FIRST; ++j) load_piece(x, 0, 0, j);
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) mbar_init(&bars[i], i == 0 && p.stall ? 2 : 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[i], i == 0 && p.stall ? 2 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -186,225 +191,213 @@ gated_grads_tc_kernel(const GradArgs p) {
   const bool kside = quad < 2;                       // rows of dK; else of dQ
   const int t = row & 63;
   const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+  const float* vec = reinterpret_cast<const float*>(smem + L::VECS);
+  const float *EG = vec, *EC = vec + C, *BT = vec + 2 * C, *GS = vec + 3 * C, *GL = vec + 4 * C;
+  uint8_t* wt = smem + L::ROWS;
   float acc[HC];
   bool ok = true;
   int nhead = 0;
+  unsigned turn = 0;
+  // One thread's: the products with piece j, accumulated over the pieces.
+  auto products = [&](int j) {
+    constexpr uint32_t id = make_idesc_bf16(128, DK, false, true);      // the states' rows are the sum's index
+    const uint32_t rows = base + L::ROWS + (j >> 1) * L::RBOX;
+    const uint64_t hi = make_sdesc(base + at_piece(turn, j), 8192, 1024, kSwizzle128B);
+    const uint64_t lo = sdesc_add(hi, L::PART);
+    const uint64_t a = make_sdesc(rows + ((j & 1) ? L::kEh : L::kRh), 16, 1024, kSwizzle128B);
+    const uint64_t al = make_sdesc(rows + ((j & 1) ? L::kEl : L::kRl), 16, 1024, kSwizzle128B);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t d = tmem + ((j & 1) ? L::D2 : L::D1), dl = (j & 1) ? d : tmem + L::D1B;
+      const bool more = j > 1 || k > 0;
+      mma_ss(d, sdesc_add(a, k * 32), sdesc_add(hi, k * 2048), id, more);
+      mma_ss(d, sdesc_add(a, k * 32), sdesc_add(lo, k * 2048), id, true);
+      mma_ss(dl, sdesc_add(al, k * 32), sdesc_add(hi, k * 2048), id, (j & 1) ? true : more);
+    }
+  };
+  // S_0 . dS over values 64 i .., high times high and what that leaves out
+  auto dot_of = [&](int i) {
+    float d = 0.f;
+    auto add8 = [&](const uint4& a, const uint4& b) {
+      d = fmaf(low_half(a.x), low_half(b.x), fmaf(high_half(a.x), high_half(b.x), d));
+      d = fmaf(low_half(a.y), low_half(b.y), fmaf(high_half(a.y), high_half(b.y), d));
+      d = fmaf(low_half(a.z), low_half(b.z), fmaf(high_half(a.z), high_half(b.z), d));
+      d = fmaf(low_half(a.w), low_half(b.w), fmaf(high_half(a.w), high_half(b.w), d));
+    };
+    const uint8_t *s0 = smem + at_piece(turn, 2 * i), *ds = smem + at_piece(turn, 2 * i + 1);
+#pragma unroll
+    for (int e = 0; e < L::PART / 16 / NT; ++e) {
+      const int at = (tid + e * NT) * 16;
+      const uint4 a = *reinterpret_cast<const uint4*>(s0 + at), al = *reinterpret_cast<const uint4*>(s0 + L::PART + at);
+      const uint4 b = *reinterpret_cast<const uint4*>(ds + at), bl = *reinterpret_cast<const uint4*>(ds + L::PART + at);
+      add8(a, b);
+      add8(al, b);
+      add8(a, bl);
+    }
+    return d;
+  };
   while (true) {
-    const uint32_t kq = base + L::KQ + kbuf * L::KQB, rows = base + L::ROWS + buf * L::ROWB;
-    const float* vec = reinterpret_cast<const float*>(smem + L::VECS + buf * 5 * C * 4);
-    const float *EG = vec, *EC = vec + C, *BT = vec + 2 * C, *GS = vec + 3 * C, *GL = vec + 4 * C;
     const uint32_t parity = nhead & 1;
-    uint8_t* wt = smem + (L::kOver ? L::ROWS + buf * L::ROWB : L::WEXTRA);
-    const uint32_t wa = smem_addr(wt);
-
-    cp_wait<1>();                                    // this head's rows; its states may be on their way
+    cp_wait<0>();
     fence_proxy_async_smem();
     __syncthreads();
     if (tid == 0) {
-      // 1. [dR; dO] E^T
       tc_fence_after();
+      if (FIRST < L::NP) {                           // its slot is wanted first
+        products(0);
+        tc_commit(&bars[3]);
+      }
+      // 1. [dR; dO] E^T
       constexpr uint32_t id = make_idesc_bf16(128, 64, false, false);
-      const uint64_t da = make_sdesc(rows + 64 * 128, 16, 1024, kSwizzle128B), db = make_sdesc(rows, 16, 1024, kSwizzle128B);
+      const uint64_t a = make_sdesc(base + L::ROWS + L::kRh, 16, 1024, kSwizzle128B);
+      const uint64_t al = make_sdesc(base + L::ROWS + L::kRl, 16, 1024, kSwizzle128B);
+      const uint64_t b = make_sdesc(base + L::ROWS + L::kEh, 16, 1024, kSwizzle128B);
+      const uint64_t bl = make_sdesc(base + L::ROWS + L::kEl, 16, 1024, kSwizzle128B);
 #pragma unroll
       for (int k = 0; k < DV / 16; ++k) {
         const uint32_t off = (k >> 2) * L::RBOX + (k & 3) * 32;
-        mma_ss(tmem + L::D3, sdesc_add(da, off), sdesc_add(db, off), id, k > 0);
+        mma_ss(tmem + L::D3, sdesc_add(a, off), sdesc_add(b, off), id, k > 0);
+        mma_ss(tmem + L::D3, sdesc_add(a, off), sdesc_add(bl, off), id, true);
+        mma_ss(tmem + L::D3B, sdesc_add(al, off), sdesc_add(b, off), id, k > 0);
       }
       tc_commit(&bars[0]);
+      // 2. with the states
+      for (int j = FIRST < L::NP ? 1 : 0; j < FIRST; ++j) products(j);
+      if (FIRST == L::NP) tc_commit(&bars[1]);
+    }
+    float dot0 = dot_of(0);
+    if (FIRST < L::NP) {
+      ok = ok && mbar_wait(&bars[3], parity, abort_flag, kWaitNs);
+      __syncthreads();                               // (all have read it, too)
+      load_piece(x, hh, turn, FIRST);
     }
     // the next head, or the next chunk's first
     Unit nx = x;
-    int nh = hh + 1, nk = kbuf;
+    int nh = hh + 1;
     if (nh == group) {
       nx = unit_at(x.u + gridDim.x);
       nh = 0;
-      nk ^= 1;
     }
     const bool more = nx.u < p.units;
-    if (more) load_rows(nx, nh, buf ^ 1, nk);
-    if (more) cp_wait<1>(); else cp_wait<0>();       // this head's states
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      // 2. [E; dR] dS^T and [dR; dO] S_0^T: the states' rows are the sum's index
-      constexpr uint32_t id = make_idesc_bf16(128, DK, false, true);
-      const uint64_t de = make_sdesc(rows, 16, 1024, kSwizzle128B), dr = make_sdesc(rows + 64 * 128, 16, 1024, kSwizzle128B);
-      const uint64_t ds = make_sdesc(base + L::DS, L::SBOX, 1024, kSwizzle128B);
-      const uint64_t s0 = make_sdesc(base + L::S0, L::SBOX, 1024, kSwizzle128B);
-#pragma unroll
-      for (int k = 0; k < DV / 16; ++k)
-        mma_ss(tmem + L::D2, sdesc_add(de, (k >> 2) * L::RBOX + (k & 3) * 32), sdesc_add(ds, k * 2048), id, k > 0);
-#pragma unroll
-      for (int k = 0; k < DV / 16; ++k)
-        mma_ss(tmem + L::D1, sdesc_add(dr, (k >> 2) * L::RBOX + (k & 3) * 32), sdesc_add(s0, k * 2048), id, k > 0);
-      tc_commit(&bars[1]);
-    }
-    float dot0 = 0.f;                                // S_0 . dS
-    auto add8 = [&](const uint4& a, const uint4& b) {
-      dot0 = fmaf(low_half(a.x), low_half(b.x), fmaf(high_half(a.x), high_half(b.x), dot0));
-      dot0 = fmaf(low_half(a.y), low_half(b.y), fmaf(high_half(a.y), high_half(b.y), dot0));
-      dot0 = fmaf(low_half(a.z), low_half(b.z), fmaf(high_half(a.z), high_half(b.z), dot0));
-      dot0 = fmaf(low_half(a.w), low_half(b.w), fmaf(high_half(a.w), high_half(b.w), dot0));
-    };
-#pragma unroll 4
-    for (int i = 0; i < DK * DV / 8 / NT; ++i)
-      add8(*reinterpret_cast<const uint4*>(smem + L::S0 + (tid + i * NT) * 16),
-           *reinterpret_cast<const uint4*>(smem + L::DS + (tid + i * NT) * 16));
-    if (p.states_lo != nullptr) {
-      const long long at = ((long long)x.slot * p.H + x.hk * group + hh) * DK * DV;
-#pragma unroll 2
-      for (int i = 0; i < DV * KCH / NT; ++i) {
-        const int j = tid + i * NT;
-        const uint32_t pos = box_at(j / KCH, j % KCH, L::SBOX);
-        const uint4 a = *reinterpret_cast<const uint4*>(p.states_lo + at + j * 8);
-        const uint4 b = *reinterpret_cast<const uint4*>(p.dstates_lo + at + j * 8);
-        add8(*reinterpret_cast<const uint4*>(smem + L::S0 + pos), b);
-        add8(a, *reinterpret_cast<const uint4*>(smem + L::DS + pos));
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot0 += __shfl_xor_sync(0xffffffffu, dot0, o);
-    if (lane == 0) dots[warp] = dot0;
-    // N or W of this row, columns j = 16 part .., as bf16
+    // N or W of this row, columns j = 16 part ..
     const float eg = EG[t], ec = EC[t], bt = BT[t], gs = GS[t], gl = GL[t];
-    uint32_t w16[8];
+    float nw[16];
     ok = ok && mbar_wait(&bars[0], parity, abort_flag, kWaitNs);
     tc_fence_after();
     {
-      uint32_t v[16];
+      uint32_t v[16], w[16];
       tmem_ld16(lanes + L::D3 + 16 * part, v);
+      if (kside) tmem_ld16(lanes + L::D3B + 16 * part, w);
       tmem_ld_wait();
       const float f = kside ? -1.f : p.scale;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j0 = 16 * part + 4 * i;
         const float4 g4 = *reinterpret_cast<const float4*>(GS + j0), l4 = *reinterpret_cast<const float4*>(GL + j0);
-        const float4 b4 = *reinterpret_cast<const float4*>(BT + j0);
-        const float gj[4] = {g4.x, g4.y, g4.z, g4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w}, bj[4] = {b4.x, b4.y, b4.z, b4.w};
-        float a[4];
+        const float gj[4] = {g4.x, g4.y, g4.z, g4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float d;
           asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"((gs - gj[e]) + (gl - lj[e])));
-          const float w = f * bj[e] * __uint_as_float(v[4 * i + e]);
-          a[e] = j0 + e < t ? d * w : j0 + e == t && !kside ? w : 0.f;
+          const float y = f * (kside ? __uint_as_float(v[4 * i + e]) + __uint_as_float(w[4 * i + e]) : __uint_as_float(v[4 * i + e]));
+          nw[4 * i + e] = j0 + e < t ? d * y : j0 + e == t && !kside ? y : 0.f;
         }
-        w16[2 * i] = pack2(a[0], a[1]);
-        w16[2 * i + 1] = pack2(a[2], a[3]);
       }
     }
+    if (FIRST < L::NP) {
+      cp_wait<0>();
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0) {
+        products(FIRST);
+        tc_commit(&bars[1]);
+      }
+      dot0 += dot_of(1);
+    } else if (L::NP == 4) {
+      dot0 += dot_of(1);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot0 += __shfl_xor_sync(0xffffffffu, dot0, o);
+    if (lane == 0) dots[warp] = dot0;
     ok = ok && mbar_wait(&bars[1], parity, abort_flag, kWaitNs);
     tc_fence_after();
-    // (a barrier: the states, E, dR and dO have been read by all)
-    const bool tiny = __syncthreads_or(fabsf(bt) < kTiny);
-    if (more) load_states(nx, nh);
-    // [N; W] by rows, [N^T W^T] by columns
+    if (hh == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint4*>(wt + box_at(row, 2 * part + i, 0)) =
-          make_uint4(w16[4 * i], w16[4 * i + 1], w16[4 * i + 2], w16[4 * i + 3]);
-    if (tiny) {
-      uint32_t v[16];
-      tmem_ld16(lanes + L::D3 + 16 * part, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = 16 * part + i;
-        if (!(fabsf(BT[j]) < kTiny)) continue;
-        float d;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"((gs - GS[j]) + (gl - GL[j])));
-        const float w = (kside ? -kTiny : kTiny * p.scale) * __uint_as_float(v[i]);
-        const uint32_t one = pack2(j < t ? d * w : j == t && !kside ? w : 0.f, 0.f);
-        w16[i >> 1] = (i & 1) ? (w16[i >> 1] & 0xffffu) | (one << 16) : (w16[i >> 1] & 0xffff0000u) | one;
-      }
+      for (int i = 0; i < HC; ++i) acc[i] = 0.f;
     }
-    {
-      uint8_t* to = wt + 16384 + (kside ? 0 : 8192) + 2 * (t & 7);
+    // This row of K or Q against the products: sums of the row's products, factors after
+    // the sums. dR's low part times S_0 first, whose columns step 3 takes.
+    float d1 = 0.f, d3 = 0.f, d5 = 0.f, d2 = 0.f;
+    const uint8_t* xr = smem + L::KQ;
+    const float f1 = kside ? -eg : p.scale * eg, f3 = bt * ec;
+    auto against = [&](uint32_t cols, float f, float& sum) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = 16 * part + i;
-        const uint32_t w = w16[i >> 1];
-        *reinterpret_cast<uint16_t*>(to + j * 128 + (((t >> 3) ^ (j & 7)) << 4)) = (uint16_t)((i & 1) ? w >> 16 : w);
+      for (int c0 = 0; c0 < HC; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(lanes + cols + part * HC + c0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 r4 = *reinterpret_cast<const uint4*>(xr + box_at(row, (part * HC + c0) / 8 + i, L::KBOX));
+          const uint32_t r[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = __uint_as_float(v[8 * i + e]);
+            acc[c0 + 8 * i + e] = fmaf(f, a, acc[c0 + 8 * i + e]);
+            sum = fmaf((e & 1) ? high_half(r[e >> 1]) : low_half(r[e >> 1]), a, sum);
+          }
+        }
+      }
+    };
+    if (kside) against(L::D1B, f1, d1);
+    __syncthreads();                                 // (E, dR, dO and the states have been read by all)
+    // [N; W] and [N; W] beta by rows, as they are multiplied from both sides
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 bj = *reinterpret_cast<const float2*>(BT + 16 * part + 2 * i);
+        split2(nw[2 * i] * (b ? bj.x : 1.f), nw[2 * i + 1] * (b ? bj.y : 1.f), hi[i], lo[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t at = 2 * b * L::TILE + box_at(row, 2 * part + i, 0);
+        *reinterpret_cast<uint4*>(wt + at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+        *reinterpret_cast<uint4*>(wt + L::TILE + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
       }
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
-      // 3. [N; W] K and [N^T W^T] [K; Q]: tokens are the sum's index
+      // 3. [N; W] beta K and [N; W]^T [K; Q]: tokens are the sum's index
       tc_fence_after();
-      constexpr uint32_t id = make_idesc_bf16(128, DK, false, true);
-      const uint64_t dw = make_sdesc(wa, 16, 1024, kSwizzle128B), dt = make_sdesc(wa + 16384, 16, 1024, kSwizzle128B);
-      const uint64_t dkq = make_sdesc(kq, L::KBOX, 1024, kSwizzle128B);
+      constexpr uint32_t id = make_idesc_bf16(128, DK, false, true), idt = make_idesc_bf16(128, DK, true, true);
+      const uint64_t dkq = make_sdesc(base + L::KQ, L::KBOX, 1024, kSwizzle128B);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mma_ss(tmem + L::D5A, sdesc_add(dw, k * 32), sdesc_add(dkq, k * 2048), id, k > 0);
+      for (int lo = 0; lo < 2; ++lo) {
+        const uint64_t a = make_sdesc(base + L::ROWS + (2 + lo) * L::TILE, 16, 1024, kSwizzle128B);
+        // (rows 64 .. 127 of the transposed: the next tile's, into the unused lanes)
+        const uint64_t at = make_sdesc(base + L::ROWS + lo * L::TILE, L::TILE, 1024, kSwizzle128B);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mma_ss(tmem + L::D5B, sdesc_add(dt, (k >> 2) * 8192 + (k & 3) * 32), sdesc_add(dkq, k * 2048), id, k > 0);
+        for (int k = 0; k < 4; ++k) mma_ss(tmem + L::D5A, sdesc_add(a, k * 32), sdesc_add(dkq, k * 2048), id, lo > 0 || k > 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ss(tmem + L::D5B, sdesc_add(at, k * 2048), sdesc_add(dkq, k * 2048), idt, lo > 0 || k > 0);
+      }
       tc_commit(&bars[2]);
     }
-    // this row of K or Q against what has come so far
-    if (hh == 0) {
-#pragma unroll
-      for (int i = 0; i < HC; ++i) acc[i] = 0.f;
-    }
-    // (sums of the row's products, factors after the sums)
-    float d1 = 0.f, d3 = 0.f, d5 = 0.f, d2 = 0.f;
-    const uint8_t* xr = smem + (kq - base);
-    const float f1 = kside ? -eg : p.scale * eg, f3 = bt * ec;
-#pragma unroll
-    for (int c0 = 0; c0 < HC; c0 += 16) {
-      uint32_t v[16], w[16];
-      tmem_ld16(lanes + L::D1 + part * HC + c0, v);
-      if (kside) tmem_ld16(lanes + L::D2 + part * HC + c0, w);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 r4 = *reinterpret_cast<const uint4*>(xr + box_at(row, (part * HC + c0) / 8 + i, L::KBOX));
-        const uint32_t r[4] = {r4.x, r4.y, r4.z, r4.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xv = (e & 1) ? high_half(r[e >> 1]) : low_half(r[e >> 1]), a = __uint_as_float(v[8 * i + e]);
-          float& y = acc[c0 + 8 * i + e];
-          y = fmaf(f1, a, y);
-          d1 = fmaf(xv, a, d1);
-          if (kside) {
-            const float b = __uint_as_float(w[8 * i + e]);
-            y = fmaf(f3, b, y);
-            d3 = fmaf(xv, b, d3);
-          }
-        }
-      }
-    }
+    if (more)
+      for (int j = 0; j < FIRST; ++j) load_piece(nx, nh, turn + L::NP, j);
+    against(L::D1, f1, d1);
+    if (kside) against(L::D2, f3, d3);
     ok = ok && mbar_wait(&bars[2], parity, abort_flag, kWaitNs);
     tc_fence_after();
-    const float f5 = fabsf(bt) < kTiny ? bt * kHuge : 1.f;
-#pragma unroll
-    for (int c0 = 0; c0 < HC; c0 += 16) {
-      uint32_t v[16], w[16];
-      tmem_ld16(lanes + L::D5A + part * HC + c0, v);
-      if (kside) tmem_ld16(lanes + L::D5B + part * HC + c0, w);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 r4 = *reinterpret_cast<const uint4*>(xr + box_at(row, (part * HC + c0) / 8 + i, L::KBOX));
-        const uint32_t r[4] = {r4.x, r4.y, r4.z, r4.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xv = (e & 1) ? high_half(r[e >> 1]) : low_half(r[e >> 1]), a = __uint_as_float(v[8 * i + e]);
-          float& y = acc[c0 + 8 * i + e];
-          y += a;
-          d2 = fmaf(xv, a, d2);
-          if (kside) {
-            const float b = __uint_as_float(w[8 * i + e]);
-            y = fmaf(f5, b, y);
-            d5 = fmaf(xv, b, d5);
-          }
-        }
-      }
-    }
+    against(L::D5A, 1.f, d2);
+    if (kside) against(L::D5B, bt, d5);
     tc_fence_before();
-    float* sums = reinterpret_cast<float*>(wt + 32768);        // [quarter][d1 of both sides, d3, d5]
+    float* sums = reinterpret_cast<float*>(wt + L::SUMS);      // [quarter][f1 d1 + d2 of both sides, d3, d5]
     sums[part * 256 + row] = fmaf(f1, d1, d2);
     if (kside) {
       sums[part * 256 + 128 + t] = ec * d3;
@@ -440,11 +433,9 @@ gated_grads_tc_kernel(const GradArgs p) {
       float xg[2], xb[2], ws = lane < NT / 32 ? EG[C - 1] * dots[lane] : 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const bool small = fabsf(b[e]) < kTiny;
-        xb[e] = s3[e] + __fdividef(s5[e], small ? kTiny : b[e]);
-        const float w = b[e] * s3[e];
-        ws += w;
-        xg[e] = s0[e] - w - (small ? b[e] * kHuge * s5[e] : s5[e]);
+        xb[e] = s3[e] + s5[e];
+        ws += b[e] * s3[e];
+        xg[e] = s0[e] - b[e] * xb[e];
       }
       // from each token to the end, and what the end's sum carries (ws) for all
       float s = xg[0] + xg[1];
@@ -474,17 +465,20 @@ gated_grads_tc_kernel(const GradArgs p) {
       }
     }
     if (!more) break;
-    x = nx; hh = nh; kbuf = nk; buf ^= 1;
+    __syncthreads();                                 // the sums, the rows on their way out and K, Q have been read
+    load_rows(nx, nh);
+    x = nx; hh = nh;
+    turn += L::NP;
     ++nhead;
   }
   // copies and products in flight end before shared and tensor memory are released
   cp_wait<0>();
   if (*abort_flag) {
     if (tid == 0) {
-      mbar_init(&bars[3], 1);
+      mbar_init(&bars[4], 1);
       fence_mbar_init();
-      tc_commit(&bars[3]);
-      mbar_drain(&bars[3], 0, kWaitNs);
+      tc_commit(&bars[4]);
+      mbar_drain(&bars[4], 0, kWaitNs);
       atomicExch(p.status, (int)LA_ERR_TIMEOUT);
     }
   }
@@ -507,24 +501,14 @@ cudaError_t launch(const GradArgs& p, cudaStream_t stream) {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// A chunk's and head's dg share one product, e^{G_C} S_0.dS, of dk dv terms: with
-// both factors rounded to bf16 it is off by about 2^-9 of the root of its squared terms'
-// sum, as much as the product itself where they cancel. Over many chunks and
-// heads that stays near 2^-9 of dg's 2-norm; with few of them the states' low parts are
-// kept for it too: largest of 12 draws 4.5e-3 of dg's norm against 5.6e-3 at 4 heads
-// of 512 tokens (32 chunks), the same 3.7e-3 at 64 chunks, where it costs a tenth of the time.
-constexpr long long kFewChunks = 64;
-
-struct Parts { size_t rec, e, states, chunks; bool lo; };
+struct Parts { size_t rec, chunks, rows, states; };
 Parts parts(int B, int H, int N, int dk, int dv, int nseq, bool packed, bool backward) {
   const long long slots = chunk_slots(B, N, nseq, packed, C);
   Parts s;
   s.rec = up256((size_t)slots * H * (backward ? REC_BWD : REC_FWD));
   s.chunks = backward ? up256((size_t)slots * sizeof(int4)) : 0;
-  s.e = up256((size_t)B * H * N * dv * 2);
+  s.rows = up256((size_t)B * H * N * dv * 2);
   s.states = up256((size_t)slots * H * dk * dv * 2);
-  // (the size query does not know whether one batch entry is packed)
-  s.lo = chunk_slots(B, N, nseq, B == 1, C) * H <= kFewChunks;
   return s;
 }
 
@@ -536,11 +520,11 @@ size_t mma_gated_forward_workspace(int B, int H, int N, int dk, int dv, int nseq
 
 size_t mma_gated_backward_workspace(int B, int H, int N, int dk, int dv, int nseq, bool packed) {
   const Parts s = parts(B, H, N, dk, dv, nseq, packed, true);
-  return s.rec + s.chunks + s.e + (s.lo ? 4 : 2) * s.states;
+  return s.rec + s.chunks + 3 * s.rows + 4 * s.states;
 }
 
 cudaError_t mma_gated_forward(const GatedArgs& a) {
-  const cudaError_t e = gated_prep(a, (uint8_t*)a.workspace, nullptr, true);
+  const cudaError_t e = gated_prep(a, (uint8_t*)a.workspace, nullptr);
   if (e != cudaSuccess) return e;
   const uint8_t* records = (const uint8_t*)a.workspace;
   if (gated_split_wanted(a, false)) return gated_split_forward(a, records);
@@ -551,16 +535,22 @@ cudaError_t mma_gated_backward(const GatedArgs& a) {
   const Parts s = parts(a.B, a.H, a.N, a.dk, a.dv, a.nseq, a.offsets != nullptr, true);
   uint8_t* ws = (uint8_t*)a.workspace;
   int4* chunks = (int4*)(ws + s.rec);
-  __nv_bfloat16* e = (__nv_bfloat16*)(ws + s.rec + s.chunks);
-  __nv_bfloat16* st[4];                // states, their gradients, low parts of both
-  for (int i = 0; i < 4; ++i) st[i] = i < 2 || s.lo ? (__nv_bfloat16*)(ws + s.rec + s.chunks + s.e + i * s.states) : nullptr;
-  cudaError_t err = gated_prep(a, ws, chunks, a.dS0 != nullptr);
+  uint8_t* at = ws + s.rec + s.chunks;
+  auto take = [&](size_t bytes) {
+    __nv_bfloat16* x = (__nv_bfloat16*)at;
+    at += bytes;
+    return x;
+  };
+  ChainOut o;
+  o.e = take(s.rows); o.e_lo = take(s.rows); o.dr_lo = take(s.rows);
+  o.states = take(s.states); o.states_lo = take(s.states); o.dstates = take(s.states); o.dstates_lo = take(s.states);
+  cudaError_t err = gated_prep(a, ws, chunks);
   if (err != cudaSuccess) return err;
-  err = gated_split_wanted(a, true) ? gated_split_backward(a, ws, e, st) : gated_chain_backward(a, ws, e, st);
+  err = gated_split_wanted(a, true) ? gated_split_backward(a, ws, o) : gated_chain_backward(a, ws, o);
   if (err != cudaSuccess) return err;
   GradArgs p{};
-  p.q = (const __nv_bfloat16*)a.q; p.k = (const __nv_bfloat16*)a.k; p.dout = (const __nv_bfloat16*)a.dout; p.e = e;
-  p.dr = (const __nv_bfloat16*)a.dv_; p.states = st[0]; p.dstates = st[1]; p.states_lo = st[2]; p.dstates_lo = st[3]; p.rec = ws; p.chunks = chunks;
+  p.q = (const __nv_bfloat16*)a.q; p.k = (const __nv_bfloat16*)a.k; p.dout = (const __nv_bfloat16*)a.dout;
+  p.dr = (const __nv_bfloat16*)a.dv_; p.c = o; p.rec = ws; p.chunks = chunks;
   p.dq = (__nv_bfloat16*)a.dq; p.dk = (__nv_bfloat16*)a.dk_; p.dg = (__nv_bfloat16*)a.dg; p.dbeta = (__nv_bfloat16*)a.dbeta;
   p.Hk = a.Hk; p.H = a.H; p.N = a.N; p.scale = a.scale;
   p.status = device_status_ptr();

@@ -26,7 +26,7 @@
 // reaches rows of bf16 once would take 232 products of 16 x 8 x 16 a chunk and 16 columns (d = 128)
 // in the place of 504, but R, the triangles and the sums over them cancel where keys are
 // alike: with cosines of 0.9 between them outputs were off by up to 2e-2 of their two-norm (3.4e-3
-// with independent keys). In the backward what reaches no dS0 goes in rounded once still.
+// with independent keys), dv and dk by as much, dg by up to 1.5e-1.
 #pragma once
 
 #include "la_gated.cuh"
@@ -46,13 +46,11 @@ constexpr int C = 64;                      // tokens per chunk
 constexpr int NB = 10;                     // 16 x 16 blocks on and below the diagonal
 constexpr int FRAG = NB * 512;             // bytes of a triangle's B fragments, bf16
 constexpr int VEC = 3 * C * 4;             // e^G, e^{G_C - G}, beta
-// A chunk's record: forward [T lo | T hi | vec | P hi | P lo]; backward [T hi | vec | T^T hi |
+// A chunk's record: [T lo | T hi | vec | P hi | P lo], backward [T lo | T hi | vec | T^T hi |
 // P^T hi | T^T lo | P^T lo | G / log 2 as two fp32].
 constexpr int REC_FWD = 4 * FRAG + VEC;
-constexpr int REC_BWD = 5 * FRAG + VEC + 2 * C * 4;
-__host__ __device__ constexpr int off_vec(bool backward) { return backward ? FRAG : 2 * FRAG; }
-__host__ __device__ constexpr int off_rest(bool backward) { return off_vec(backward) + VEC; }
-constexpr int OFF_SUMS = 5 * FRAG + VEC;
+constexpr int OFF_VEC = 2 * FRAG, OFF_REST = OFF_VEC + VEC, OFF_SUMS = OFF_REST + 4 * FRAG;
+constexpr int REC_BWD = OFF_SUMS + 2 * C * 4;
 
 __device__ __forceinline__ int block_of(int i, int j) { return i * (i + 1) / 2 + j; }   // row block i >= j
 
@@ -117,6 +115,13 @@ __device__ __forceinline__ void rows_to(uint32_t (&m)[4], const uint32_t (&a)[4]
   }
 }
 
+// As split2, the high parts as a rounding to bf16 has them (infinite beyond bf16's
+// largest number): rows that the caller gets.
+__device__ __forceinline__ void split2_out(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(a, b);
+  lo = pack2(a - low_half(hi), b - high_half(hi));
+}
+
 // TMA copies: every wait for one is bounded
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -143,23 +148,26 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const uint8_t* src, int
 
 }  // namespace gmma
 
-// The records of every chunk slot and head (la_gated_prep.cu); lo: with the low
-// parts (a state is asked for); chunks given: those of the backward, with the transposed
-// triangles, and every slot's batch entry, first row and number of tokens.
-cudaError_t gated_prep(const GatedArgs& a, uint8_t* records, int4* chunks, bool lo);
-// The chains over them (la_gated_chain.cu). Backward: e [B,H,N,dv], the states
-// before and their gradients behind each chunk, [slot,H,dv,dk], bf16 (one rounding of
-// what the gradients' products take as bf16 operands), and what these two leave out (or null).
+// The records of every chunk slot and head (la_gated_prep.cu); chunks given: those of the
+// backward, with the transposed triangles, and every slot's batch entry, first row and
+// number of tokens.
+cudaError_t gated_prep(const GatedArgs& a, uint8_t* records, int4* chunks);
+// What the backward's chains leave for the gradients' products, as bf16 high and low parts:
+// E and dR [B,H,N,dv] (the high part of dR is the gradient dv), the states before and
+// their gradients behind each chunk [slot,H,dv,dk].
+struct ChainOut {
+  __nv_bfloat16 *e, *e_lo, *dr_lo;
+  __nv_bfloat16 *states, *states_lo, *dstates, *dstates_lo;
+};
+// The chains over the records (la_gated_chain.cu).
 cudaError_t gated_chain_forward(const GatedArgs& a, const uint8_t* records);
-cudaError_t gated_chain_backward(const GatedArgs& a, const uint8_t* records, __nv_bfloat16* e,
-                                 __nv_bfloat16* const (&states)[4]);
+cudaError_t gated_chain_backward(const GatedArgs& a, const uint8_t* records, const ChainOut& o);
 // The forward ones by two warps for 16 columns (la_gated_pair.cu), and whether they are taken.
 cudaError_t gated_pair_forward(const GatedArgs& a, const uint8_t* records);
 bool gated_pair_wanted(const GatedArgs& a);
 // The same for few heads, eight warps on 16 columns (la_gated_split.cu).
 cudaError_t gated_split_forward(const GatedArgs& a, const uint8_t* records);
-cudaError_t gated_split_backward(const GatedArgs& a, const uint8_t* records, __nv_bfloat16* e,
-                                 __nv_bfloat16* const (&states)[4]);
+cudaError_t gated_split_backward(const GatedArgs& a, const uint8_t* records, const ChainOut& o);
 // Whether they are taken.
 bool gated_split_wanted(const GatedArgs& a, bool backward);
 // A tensor map of [heads][N][d] bf16 in boxes of `cols` columns (16: rows of 32 bytes,

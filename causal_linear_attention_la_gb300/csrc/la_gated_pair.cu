@@ -45,7 +45,7 @@ struct PairSmem {
   // for the chain: K, the CTA's columns of V, [T lo | T hi | vec]
   static constexpr int V = TB;
   static constexpr int R = V + C * W * 32;
-  static constexpr int VA = off_vec(false);          // vec in it
+  static constexpr int VA = OFF_VEC;          // vec in it
   static constexpr int RA = VA + VEC;
   static constexpr int up(int x) { return (x + 1023) / 1024 * 1024; }   // (the swizzle goes by the address)
   static constexpr int A_BYTES = R + RA, A = up(A_BYTES);
@@ -125,7 +125,7 @@ gated_pair_kernel(const PairArgs p, const __grid_constant__ PairMaps maps) {
         const int t0 = sq.lo + i * C, at = L::AT_B + (i & 1) * L::B;
 #pragma unroll
         for (int x = 0; x < DK / 64; ++x) tma_load_3d(smem + at + x * C * 128, &maps.q, bar, 64 * x, t0, kh);
-        bulk_load(base + at + L::TB, rec + (long long)i * p.H * REC_FWD + off_vec(false), L::RB, bar);
+        bulk_load(base + at + L::TB, rec + (long long)i * p.H * REC_FWD + OFF_VEC, L::RB, bar);
       }
     };
     // Copies have whole boxes: rows behind the sequence's last token become zeros.

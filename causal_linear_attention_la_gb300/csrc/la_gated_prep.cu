@@ -56,7 +56,6 @@ struct PrepArgs {
   int4* chunks;                       // backward
   int Hk, H, N, nseq;
   float scale;
-  int lo;                             // backward: low parts of T^T and P^T wanted
 };
 
 // Four values of a 16 x 16 block as the B fragments of its two 8-column tiles.
@@ -229,7 +228,7 @@ gated_prep_kernel(const PrepArgs p) {
       __syncthreads();
     }
     const float *gs = sm.gs[hs], *gl = sm.gl[hs], *beta = sm.beta[hs];
-    float* vec = reinterpret_cast<float*>(rec + off_vec(kBackward));
+    float* vec = reinterpret_cast<float*>(rec + OFF_VEC);
     if (tid < C) {
       vec[tid] = sm.eg[hs][tid];
       vec[C + tid] = sm.ec[hs][tid];
@@ -239,16 +238,15 @@ gated_prep_kernel(const PrepArgs p) {
         reinterpret_cast<float*>(rec + OFF_SUMS)[C + tid] = gl[tid];
       }
     }
-    // T, as pairs of columns of a row, B[k = j][n = t] (the backward's chain forward takes
-    // it rounded once), and for the backward pairs of rows of a column
+    // T, as pairs of columns of a row, B[k = j][n = t], and for the backward pairs of rows of
+    // a column
     auto store_t = [&](int block, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
-      store_frag(rec + (kBackward ? 0 : FRAG), block, lane, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      if (!kBackward) store_frag(rec, block, lane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      store_frag(rec + FRAG, block, lane, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      store_frag(rec, block, lane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       if (kBackward) {
-        store_frag(rec + off_rest(true), block, lane, make_uint4(transposed(hi[0]), transposed(hi[2]), transposed(hi[1]), transposed(hi[3])));
-        if (p.lo)
-          store_frag(rec + off_rest(true) + 2 * FRAG, block, lane,
-                     make_uint4(transposed(lo[0]), transposed(lo[2]), transposed(lo[1]), transposed(lo[3])));
+        store_frag(rec + OFF_REST, block, lane, make_uint4(transposed(hi[0]), transposed(hi[2]), transposed(hi[1]), transposed(hi[3])));
+        store_frag(rec + OFF_REST + 2 * FRAG, block, lane,
+                   make_uint4(transposed(lo[0]), transposed(lo[2]), transposed(lo[1]), transposed(lo[3])));
       }
     };
     const int t0 = 16 * warp + g;          // this lane's rows: t0, t0 + 8
@@ -288,8 +286,8 @@ gated_prep_kernel(const PrepArgs p) {
         }
       }
       if (!kBackward) {
-        store_frag(rec + off_rest(false), block_of(warp, jb), lane, make_uint4(w[0], w[1], w[2], w[3]));
-        store_frag(rec + off_rest(false) + FRAG, block_of(warp, jb), lane, make_uint4(wl[0], wl[1], wl[2], wl[3]));
+        store_frag(rec + OFF_REST, block_of(warp, jb), lane, make_uint4(w[0], w[1], w[2], w[3]));
+        store_frag(rec + OFF_REST + FRAG, block_of(warp, jb), lane, make_uint4(wl[0], wl[1], wl[2], wl[3]));
       }
     };
 #pragma unroll
@@ -315,8 +313,8 @@ gated_prep_kernel(const PrepArgs p) {
             split2(t > j ? d0 * q0 : t == j ? q0 : 0.f, t + 1 > j ? d1 * q1 : t + 1 == j ? q1 : 0.f, ph[2 * r + half], pl[2 * r + half]);
           }
         }
-        store_frag(rec + off_rest(true) + FRAG, block_of(tb, warp), lane, make_uint4(ph[0], ph[1], ph[2], ph[3]));
-        if (p.lo) store_frag(rec + off_rest(true) + 3 * FRAG, block_of(tb, warp), lane, make_uint4(pl[0], pl[1], pl[2], pl[3]));
+        store_frag(rec + OFF_REST + FRAG, block_of(tb, warp), lane, make_uint4(ph[0], ph[1], ph[2], ph[3]));
+        store_frag(rec + OFF_REST + 3 * FRAG, block_of(tb, warp), lane, make_uint4(pl[0], pl[1], pl[2], pl[3]));
       }
     }
     __syncwarp();
@@ -516,11 +514,11 @@ cudaError_t launch(const PrepArgs& p, long long slots, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t gated_prep(const GatedArgs& a, uint8_t* records, int4* chunks, bool lo) {
+cudaError_t gated_prep(const GatedArgs& a, uint8_t* records, int4* chunks) {
   const bool backward = chunks != nullptr;
   PrepArgs p{};
   p.q = (const __nv_bfloat16*)a.q; p.k = (const __nv_bfloat16*)a.k; p.g = a.g; p.beta = a.beta; p.offsets = a.offsets;
-  p.rec = records; p.chunks = chunks; p.Hk = a.Hk; p.H = a.H; p.N = a.N; p.nseq = a.nseq; p.scale = a.scale; p.lo = lo;
+  p.rec = records; p.chunks = chunks; p.Hk = a.Hk; p.H = a.H; p.N = a.N; p.nseq = a.nseq; p.scale = a.scale;
   const long long slots = chunk_slots(a.B, a.N, a.nseq, a.offsets != nullptr, C);
   if (slots == 0) return cudaSuccess;
   if (a.dk == 64) return backward ? launch<64, true>(p, slots, a.stream) : launch<64, false>(p, slots, a.stream);

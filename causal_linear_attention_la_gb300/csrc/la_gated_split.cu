@@ -35,16 +35,16 @@ using sm100::tma_load_3d;
 enum { kFwd = 0, kSave = 1, kRev = 2 };
 constexpr int NH = 128;                              // helper threads, as many chain threads
 
-template <int DK, int MODE, bool LO>
+template <int DK, int MODE>
 struct SplitSmem {
   static constexpr int TB = C * DK * 2;              // a tile of K or Q
   static constexpr int VB = C * 32;                  // 16 columns of V or dO
   static constexpr int up(int x) { return (x + 1023) / 1024 * 1024; }   // (the swizzle goes by the address)
   // copies for the chain: K, (forward: V, backward: Q), T's triangles, vec
-  static constexpr int TRI = (LO ? 2 : 1) * FRAG;    // (forward: LO)
+  static constexpr int TRI = 2 * FRAG;
   static constexpr int A_X = TB;                     // V or Q
   static constexpr int A_T = A_X + (MODE == kRev ? TB : VB);
-  static constexpr int A_VEC = A_T + (MODE == kSave ? FRAG : TRI);
+  static constexpr int A_VEC = A_T + TRI;
   static constexpr int A_BYTES = A_VEC + VEC, A = up(A_BYTES);
   // and for the helpers: Q and P; backward dO and P^T's triangles; vec
   static constexpr int B_P = MODE == kRev ? VB : TB;
@@ -54,8 +54,8 @@ struct SplitSmem {
   static constexpr int SHARES = 0;                   // [to][from, without itself][2 tiles][lane] float4
   static constexpr int FR = SHARES + 12 * 1024;      // R's fragments [block][hi, lo][lane] 16 bytes
   static constexpr int FU = FR + 4096;               // and those of e^{G_C-G} U, or -e^G dR
-  static constexpr int ROWS = FU + 4096;             // two chunks' U [hi, lo][block][lane] 16 bytes, or E or dR, rounded
-  static constexpr int ROWB = MODE == kFwd ? 4096 : 2048;
+  static constexpr int ROWS = FU + 4096;             // two chunks' U, E or dR: [hi, lo][block][lane] 16 bytes
+  static constexpr int ROWB = 4096;
   static constexpr int SF = ROWS + 2 * ROWB;         // two chunks' S^T: [hi, lo][DK / 16][lane] 16 bytes
   static constexpr int SFB = 2 * (DK / 16) * 512;
   static constexpr int PRE = SF + 2 * SFB;           // backward, three chunks': P^T dO [block][2][lane] float4,
@@ -75,8 +75,9 @@ struct SplitArgs {
   const float* S_in; float* S_out;
   const int* offsets;
   __nv_bfloat16* out;                    // O, E or dR rows [B,H,N,dv]
+  __nv_bfloat16* out_lo;                 // E, dR: what that leaves out
   __nv_bfloat16* states;                 // [slot,H,dv,DK]: before each chunk (save), behind it (reverse)
-  __nv_bfloat16* states_lo;              // what that leaves out, or null
+  __nv_bfloat16* states_lo;              // what that leaves out
   int Hk, H, N, dv, nseq, nblk;
   float scale;
   int* status;
@@ -88,9 +89,9 @@ struct SplitMaps { CUtensorMap q, k, v; };
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
-template <int DK, int MODE, bool LO, bool ORDER>
+template <int DK, int MODE, bool ORDER>
 __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps& maps, long long block, uint8_t* smem) {
-  using L = SplitSmem<DK, MODE, LO>;
+  using L = SplitSmem<DK, MODE>;
   constexpr int KS = DK / 64, SA = 3 + L::DEPTH, SB = 2 + L::DEPTH;
   const int tid = threadIdx.x, lane = tid & 31, kw = (tid >> 5) & 3;
   const bool helper = tid >= NH;
@@ -104,6 +105,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
   const long long vrow = ((long long)sq.b * p.H + h) * p.N + sq.lo;
   const int m0 = blk * 16;
   __nv_bfloat16* ob = p.out + vrow * p.dv + m0;
+  __nv_bfloat16* ol = MODE == kFwd ? nullptr : p.out_lo + vrow * p.dv + m0;
   const uint32_t base = smem_addr(smem);
   const uint32_t a0 = base + L::X, b0 = a0 + SA * L::A;
   auto chunk_of = [&](int i) { return MODE == kRev ? nchunks - 1 - i : i; };
@@ -136,14 +138,12 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       if (MODE == kRev) boxes(to + L::A_X, &maps.q, t0, bar);
       else tma_load_3d(smem + (to - base) + L::A_X, &maps.v, bar, m0, sq.lo + t0, vh);
       const uint8_t* rec = p.rec + ((long long)(sq.slot + c) * p.H + h) * p.rec_bytes;
-      if (MODE == kFwd) {                            // [T lo | T hi | vec]
+      if (MODE != kRev) {                            // [T lo | T hi | vec]
         bulk_load(to + L::A_T, rec, L::TRI + VEC, bar);
-      } else if (MODE == kSave) {                    // [T hi | vec]
-        bulk_load(to + L::A_T, rec, FRAG + VEC, bar);
       } else {                                       // T^T hi, T^T lo, vec
-        bulk_load(to + L::A_T, rec + off_rest(true), FRAG, bar);
-        if (LO) bulk_load(to + L::A_T + FRAG, rec + off_rest(true) + 2 * FRAG, FRAG, bar);
-        bulk_load(to + L::A_VEC, rec + off_vec(true), VEC, bar);
+        bulk_load(to + L::A_T, rec + OFF_REST, FRAG, bar);
+        bulk_load(to + L::A_T + FRAG, rec + OFF_REST + 2 * FRAG, FRAG, bar);
+        bulk_load(to + L::A_VEC, rec + OFF_VEC, VEC, bar);
       }
     };
     auto load_b = [&](int i, uint64_t* bar) {
@@ -153,13 +153,13 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       const uint8_t* rec = p.rec + ((long long)(sq.slot + c) * p.H + h) * p.rec_bytes;
       if (MODE == kFwd) {
         boxes(to, &maps.q, t0, bar);
-        bulk_load(to + L::B_P, rec + off_rest(false), L::TRI, bar);
+        bulk_load(to + L::B_P, rec + OFF_REST, L::TRI, bar);
       } else {
         tma_load_3d(smem + (to - base), &maps.v, bar, m0, sq.lo + t0, vh);
-        bulk_load(to + L::B_P, rec + off_rest(true) + FRAG, FRAG, bar);
-        if (LO) bulk_load(to + L::B_P + FRAG, rec + off_rest(true) + 3 * FRAG, FRAG, bar);
+        bulk_load(to + L::B_P, rec + OFF_REST + FRAG, FRAG, bar);
+        bulk_load(to + L::B_P + FRAG, rec + OFF_REST + 3 * FRAG, FRAG, bar);
       }
-      bulk_load(to + L::B_VEC, rec + off_vec(MODE == kRev), VEC, bar);
+      bulk_load(to + L::B_VEC, rec + OFF_VEC, VEC, bar);
     };
     // Copies have whole boxes: rows behind the sequence's last token become zeros.
     auto clear = [&](uint32_t to, int piece, int rows0) {         // rows of `piece` 16-byte pieces
@@ -223,7 +223,6 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
         const uint4 ph = *reinterpret_cast<const uint4*>(sp + L::B_P + block_of(tb, kw) * 512 + lane * 16);
         mma(d1[0], a, ph.x, ph.y);
         mma(d1[1], a, ph.z, ph.w);
-        if (!LO) continue;
         const uint4 pl = *reinterpret_cast<const uint4*>(sp + L::B_P + FRAG + block_of(tb, kw) * 512 + lane * 16);
         mma(d2[0], a, pl.x, pl.y);
         mma(d2[1], a, pl.z, pl.w);
@@ -240,7 +239,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
         split2(p.scale * eg.x * low_half(v[e]), p.scale * eg.y * high_half(v[e]), qh[e], ql[e]);
       }
       *quad(at + 4096 + kw * 1024) = make_uint4(qh[0], qh[1], qh[2], qh[3]);
-      if (LO) *quad(at + 4096 + kw * 1024 + 512) = make_uint4(ql[0], ql[1], ql[2], ql[3]);
+      *quad(at + 4096 + kw * 1024 + 512) = make_uint4(ql[0], ql[1], ql[2], ql[3]);
     };
     // Copies that are asked for behind the barrier of chunk i: the chain's of chunk
     // i + 2 + DEPTH, over those of chunk i - 1; the helpers' of chunk i + 1 + DEPTH, or
@@ -303,7 +302,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
           }
         };
         dump(p.states, 0);
-        if (p.states_lo != nullptr) dump(p.states_lo, 1);
+        dump(p.states_lo, 1);
       }
       uint4 row4;
       {
@@ -391,16 +390,18 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
           row4 = make_uint4(pack2(y[0][0], y[0][1]), pack2(y[0][2], y[0][3]), pack2(y[1][0], y[1][1]), pack2(y[1][2], y[1][3]));
         }
       }
-      // rows [token][16 columns] of block kw, 16 bytes a lane
-      const uint32_t to = base + L::OUT + kw * 512;
-      stmatrix4t(to + tile_at<2>(((mi >> 1) << 3) + ml, mi & 1), row4.x, row4.y, row4.z, row4.w);
-      __syncwarp();
-      {
+      // rows [token][16 columns] of block kw, 16 bytes a lane: rounded, and (backward) what that leaves out
+#pragma unroll
+      for (int part = 0; part < (MODE == kFwd ? 1 : 2); ++part) {
+        const uint32_t to = base + L::OUT + kw * 512;
+        if (part == 1) row4 = *reinterpret_cast<const uint4*>(smem + L::ROWS + (i & 1) * L::ROWB + 2048 + kw * 512 + lane * 16);
+        stmatrix4t(to + tile_at<2>(((mi >> 1) << 3) + ml, mi & 1), row4.x, row4.y, row4.z, row4.w);
+        __syncwarp();
         const int r = lane >> 1, half = lane & 1, t = 16 * kw + r;
         const uint4 w = *reinterpret_cast<const uint4*>(smem + L::OUT + kw * 512 + tile_at<2>(r, half));
-        if (t < cn && ok) *reinterpret_cast<uint4*>(ob + (long long)(t0 + t) * p.dv + 8 * half) = w;
+        if (t < cn && ok) *reinterpret_cast<uint4*>((part ? ol : ob) + (long long)(t0 + t) * p.dv + 8 * half) = w;
+        __syncwarp();
       }
-      __syncwarp();
       pre(i + 2);
       if (i >= L::DEPTH) {
         landed(i + 2 - L::DEPTH);
@@ -446,8 +447,8 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
     const uint32_t sa = a0 + (i % SA) * L::A;
     const uint8_t* ap = smem + (sa - base);
     const float* vec = reinterpret_cast<const float*>(ap + L::A_VEC);
-    auto frag = [&](int lo, int b) {                 // forward records have T lo first
-      const int off = MODE == kFwd && LO ? (1 - lo) * FRAG : lo * FRAG;
+    auto frag = [&](int lo, int b) {                 // (T lo is the first in a record)
+      const int off = (MODE == kRev ? lo : 1 - lo) * FRAG;
       return *reinterpret_cast<const uint4*>(ap + L::A_T + off + b * 512 + lane * 16);
     };
     float2 eg[2], ec[2], bt[2];                      // of this lane's four tokens of block kw
@@ -490,12 +491,10 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
         mma(x[2 * t], ah, b[t][0], b[t][1]);
         mma(x[2 * t + 1], ah, b[t][2], b[t][3]);
       }
-      if (LO) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          mma(x[2 * t], al, b[t][0], b[t][1]);
-          mma(x[2 * t + 1], al, b[t][2], b[t][3]);
-        }
+      for (int t = 0; t < 4; ++t) {
+        mma(x[2 * t], al, b[t][0], b[t][1]);
+        mma(x[2 * t + 1], al, b[t][2], b[t][3]);
       }
     }
     // 2. to the warps of their blocks
@@ -520,7 +519,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       if (MODE == kRev ? b < kw : b > kw) continue;
       const int at = MODE == kRev ? block_of(b, kw) : block_of(kw, b);
       th[b] = frag(0, at);
-      if (LO) tl[b] = frag(1, at);
+      tl[b] = frag(1, at);
     }
 #pragma unroll
     for (int j = 0; j < 2 * KS; ++j)
@@ -550,7 +549,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       }
     }
     *quad(L::FR + kw * 1024) = make_uint4(rh[0], rh[1], rh[2], rh[3]);
-    if (LO) *quad(L::FR + kw * 1024 + 512) = make_uint4(rl[0], rl[1], rl[2], rl[3]);
+    *quad(L::FR + kw * 1024 + 512) = make_uint4(rl[0], rl[1], rl[2], rl[3]);
     bar_sync(2, NH);
     // 3. E^T, or dR^T: three sums, for the latency of an accumulator
     float ev[2][4], e1[2][4], e2[2][4];
@@ -565,21 +564,17 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
       const uint32_t a[4] = {f.x, f.y, f.z, f.w};
       mma(ev[0], a, th[b].x, th[b].y);
       mma(ev[1], a, th[b].z, th[b].w);
-      if (LO) {
-        const uint4 f2 = *quad(L::FR + b * 1024 + 512);
-        const uint32_t a2[4] = {f2.x, f2.y, f2.z, f2.w};
-        mma(e1[0], a2, th[b].x, th[b].y);
-        mma(e1[1], a2, th[b].z, th[b].w);
-        mma(e2[0], a, tl[b].x, tl[b].y);
-        mma(e2[1], a, tl[b].z, tl[b].w);
-      }
+      const uint4 f2 = *quad(L::FR + b * 1024 + 512);
+      const uint32_t a2[4] = {f2.x, f2.y, f2.z, f2.w};
+      mma(e1[0], a2, th[b].x, th[b].y);
+      mma(e1[1], a2, th[b].z, th[b].w);
+      mma(e2[0], a, tl[b].x, tl[b].y);
+      mma(e2[1], a, tl[b].z, tl[b].w);
     }
-    if (LO) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ev[j][e] += e1[j][e] + e2[j][e];
-    }
+      for (int e = 0; e < 4; ++e) ev[j][e] += e1[j][e] + e2[j][e];
     if (MODE == kFwd) {
       // as for the outputs: a block with a row that is not finite is done again
       float bad = 0.f;
@@ -594,7 +589,6 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
           const uint4 h4 = frag(0, block_of(kw, b));
           mma(o[0][0], a, h4.x, h4.y);
           mma(o[0][1], a, h4.z, h4.w);
-          if (!LO) return;
           const uint4 l4 = frag(1, block_of(kw, b));
           mma(o[1][0], a2, h4.x, h4.y);
           mma(o[1][1], a2, h4.z, h4.w);
@@ -604,7 +598,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
 #pragma unroll
         for (int z = 0; z < 24; ++z) low[z >> 3][(z >> 2) & 1][z & 3] = 0.f;
         for (int b = 0; b < kw; ++b) {
-          const uint4 f = *quad(L::FR + b * 1024), f2 = LO ? *quad(L::FR + b * 1024 + 512) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 f = *quad(L::FR + b * 1024), f2 = *quad(L::FR + b * 1024 + 512);
           const uint32_t a[4] = {f.x, f.y, f.z, f.w}, a2[4] = {f2.x, f2.y, f2.z, f2.w};
           add(low, a, a2, b);
         }
@@ -626,7 +620,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (8 * j + 2 * tig + (e & 1) == t) ev[j][e] = LO ? o[0][j][e] + (o[1][j][e] + o[2][j][e]) : o[0][j][e];
+              if (8 * j + 2 * tig + (e & 1) == t) ev[j][e] = o[0][j][e] + (o[1][j][e] + o[2][j][e]);
         }
       }
     }
@@ -637,18 +631,18 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
         const int j = e >> 1, r = 2 * (e & 1);
         if (MODE == kRev) {
           split2(-eg[j].x * ev[j][r], -eg[j].y * ev[j][r + 1], uh[e], ul[e]);
-          w[e] = pack2(ev[j][r], ev[j][r + 1]);
+          split2_out(ev[j][r], ev[j][r + 1], w[e], w2[e]);
         } else {
           const float u0 = bt[j].x * ev[j][r], u1 = bt[j].y * ev[j][r + 1];
           split2(ec[j].x * u0, ec[j].y * u1, uh[e], ul[e]);
           if (MODE == kFwd) split2(u0, u1, w[e], w2[e]);
-          else w[e] = pack2(ev[j][r], ev[j][r + 1]);
+          else split2_out(ev[j][r], ev[j][r + 1], w[e], w2[e]);
         }
       }
       *quad(L::FU + kw * 1024) = make_uint4(uh[0], uh[1], uh[2], uh[3]);
-      if (LO) *quad(L::FU + kw * 1024 + 512) = make_uint4(ul[0], ul[1], ul[2], ul[3]);
+      *quad(L::FU + kw * 1024 + 512) = make_uint4(ul[0], ul[1], ul[2], ul[3]);
       *quad(L::ROWS + (i & 1) * L::ROWB + kw * 512) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (MODE == kFwd) *quad(L::ROWS + (i & 1) * L::ROWB + 2048 + kw * 512) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+      *quad(L::ROWS + (i & 1) * L::ROWB + 2048 + kw * 512) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
     }
     // 4. this warp's quarter of the state
     uint32_t kt[4][KS][4], qt[MODE == kRev ? 4 : 1][KS][4];
@@ -666,7 +660,7 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         f[t] = *quad(from + t * 1024);
-        if (LO) f2[t] = *quad(from + t * 1024 + 512);
+        f2[t] = *quad(from + t * 1024 + 512);
       }
     };
     auto add = [&](const uint32_t (&tile)[4][KS][4]) {
@@ -678,13 +672,11 @@ __device__ __forceinline__ void split_chain(const SplitArgs& p, const SplitMaps&
           mma(st[2 * k2], ah, tile[t][k2][0], tile[t][k2][1]);
           mma(st[2 * k2 + 1], ah, tile[t][k2][2], tile[t][k2][3]);
         }
-        if (LO) {
-          const uint32_t al[4] = {f2[t].x, f2[t].y, f2[t].z, f2[t].w};
+        const uint32_t al[4] = {f2[t].x, f2[t].y, f2[t].z, f2[t].w};
 #pragma unroll
-          for (int k2 = 0; k2 < KS; ++k2) {
-            mma(st[2 * k2], al, tile[t][k2][0], tile[t][k2][1]);
-            mma(st[2 * k2 + 1], al, tile[t][k2][2], tile[t][k2][3]);
-          }
+        for (int k2 = 0; k2 < KS; ++k2) {
+          mma(st[2 * k2], al, tile[t][k2][0], tile[t][k2][1]);
+          mma(st[2 * k2 + 1], al, tile[t][k2][2], tile[t][k2][3]);
         }
       }
     };
@@ -712,18 +704,18 @@ template <int DK, bool ORDER>
 __global__ void __launch_bounds__(2 * NH, 1)
 gated_split_kernel(const SplitArgs p, const __grid_constant__ SplitMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  split_chain<DK, kFwd, true, ORDER>(p, maps, blockIdx.x, smem);
+  split_chain<DK, kFwd, ORDER>(p, maps, blockIdx.x, smem);
 }
 
 // Both chains of the backward in one launch (order: second_chain).
-template <int DK, bool LO>
+template <int DK>
 __global__ void __launch_bounds__(2 * NH, 1)
 gated_splits_kernel(const SplitArgs rev, const __grid_constant__ SplitMaps rmaps, const SplitArgs save,
                     const __grid_constant__ SplitMaps smaps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   unsigned number;
-  if (second_chain(blockIdx.x, gridDim.x, rev.offsets != nullptr, rev.nblk * rev.H, number)) split_chain<DK, kSave, false, true>(save, smaps, number, smem);
-  else split_chain<DK, kRev, LO, true>(rev, rmaps, number, smem);
+  if (second_chain(blockIdx.x, gridDim.x, rev.offsets != nullptr, rev.nblk * rev.H, number)) split_chain<DK, kSave, true>(save, smaps, number, smem);
+  else split_chain<DK, kRev, true>(rev, rmaps, number, smem);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -745,12 +737,12 @@ bool make_maps(SplitMaps* m, const SplitArgs& a, int B, int dk) {
          gated_map(&m->v, a.v, (long long)B * a.H, a.N, a.dv, 16);
 }
 
-template <int DK, bool LO>
+template <int DK>
 cudaError_t launch(SplitArgs f, int B, const SplitArgs* save, cudaStream_t stream) {
   f.nblk = f.dv / 16;
   const long long grid = (long long)f.nseq * f.H * f.nblk * (save != nullptr ? 2 : 1);
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  constexpr int kF = SplitSmem<DK, kFwd, true>::TOTAL, kR = SplitSmem<DK, kRev, LO>::TOTAL, kS = SplitSmem<DK, kSave, false>::TOTAL;
+  constexpr int kF = SplitSmem<DK, kFwd>::TOTAL, kR = SplitSmem<DK, kRev>::TOTAL, kS = SplitSmem<DK, kSave>::TOTAL;
   cudaError_t e;
   SplitMaps fm, bm;
   if (!make_maps(&fm, f, B, DK) || (save != nullptr && !make_maps(&bm, *save, B, DK))) return cudaErrorInvalidValue;
@@ -768,7 +760,7 @@ cudaError_t launch(SplitArgs f, int B, const SplitArgs* save, cudaStream_t strea
     b.status = f.status;
     b.stall = f.stall;
     constexpr int smem = kR > kS ? kR : kS;
-    auto kern = gated_splits_kernel<DK, LO>;
+    auto kern = gated_splits_kernel<DK>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, 2 * NH, smem, stream>>>(f, fm, b, bm);
@@ -779,9 +771,7 @@ cudaError_t launch(SplitArgs f, int B, const SplitArgs* save, cudaStream_t strea
 }
 
 cudaError_t dispatch(const SplitArgs& f, const SplitArgs* save, int B, int dk, cudaStream_t stream) {
-  const bool lo = save == nullptr || f.S_out != nullptr;
-  if (dk == 64) return lo ? launch<64, true>(f, B, save, stream) : launch<64, false>(f, B, save, stream);
-  return lo ? launch<128, true>(f, B, save, stream) : launch<128, false>(f, B, save, stream);
+  return dk == 64 ? launch<64>(f, B, save, stream) : launch<128>(f, B, save, stream);
 }
 
 SplitArgs split_args(const GatedArgs& a, const uint8_t* rec, int rec_bytes) {
@@ -824,12 +814,11 @@ cudaError_t gated_split_forward(const GatedArgs& a, const uint8_t* records) {
   return dispatch(p, nullptr, a.B, a.dk, a.stream);
 }
 
-cudaError_t gated_split_backward(const GatedArgs& a, const uint8_t* records, __nv_bfloat16* e,
-                                 __nv_bfloat16* const (&states)[4]) {
+cudaError_t gated_split_backward(const GatedArgs& a, const uint8_t* records, const ChainOut& o) {
   SplitArgs r = split_args(a, records, REC_BWD), s = r;
-  r.v = (const __nv_bfloat16*)a.dout; r.S_in = a.dS; r.S_out = a.dS0; r.out = (__nv_bfloat16*)a.dv_;
-  r.states = states[1]; r.states_lo = states[3];
-  s.S_in = a.S0; s.out = e; s.states = states[0]; s.states_lo = states[2];
+  r.v = (const __nv_bfloat16*)a.dout; r.S_in = a.dS; r.S_out = a.dS0; r.out = (__nv_bfloat16*)a.dv_; r.out_lo = o.dr_lo;
+  r.states = o.dstates; r.states_lo = o.dstates_lo;
+  s.S_in = a.S0; s.out = o.e; s.out_lo = o.e_lo; s.states = o.states; s.states_lo = o.states_lo;
   return dispatch(r, &s, a.B, a.dk, a.stream);
 }
 

@@ -533,9 +533,9 @@ LA_API la_status la_state_unpack(const unsigned char* codes, const unsigned char
  * Where la_gated_delta_path is 1 (bf16, dk and dv in {64, 128}) whole sequences
  * are computed in chunks of 64 tokens on the tensor cores; fp32 operands of a
  * product go in as bf16 high and low parts (states within 1e-5 of their 2-norm on unit-norm
- * keys in random directions, within 3e-5 on keys that are nearly equal; outputs as those of fp32
- * arithmetic). Otherwise, for N <= 32, and backward for up to 1024 rows of all heads and batch entries
- * (N <= 256), token by token in fp32. The tensor core kernels' waits are bounded:
+ * keys in random directions, within 3e-5 on keys that are nearly equal; outputs and gradients
+ * within bf16's rounding of these; dg, whose terms cancel the most, within 2^-18 of the terms
+ * it is a sum of). Otherwise, and for N <= 32, token by token in fp32. The tensor core kernels' waits are bounded:
  * la_device_status has LA_ERR_TIMEOUT if one ever ran out.
  */
 LA_API int la_gated_delta_path(int dk, int dv, la_dtype dtype);
@@ -550,8 +550,7 @@ LA_API la_status la_forward_gated_delta(const void* q, const void* k, const void
 /*
  * Gradients of L = sum(dout * out) + sum(dS * S_final), out and S_final those of
  * la_forward_gated_delta: dq, dk_ [B,Hk,N,dk] (summed over the heads that
- * share them), dv_ [B,H,N,dv], dg, dbeta [B,H,N], all in dtype (with bf16 rows the
- * products behind dg and dbeta have bf16 operands, and fp32 would only look more exact);
+ * share them), dv_ [B,H,N,dv], dg, dbeta [B,H,N], all in dtype (sums in fp32, rounded once at the end);
  * dS0 [nseq,H,dk,dv] fp32 or NULL. dS [nseq,H,dk,dv] fp32 or NULL (zero); dS0
  * may be dS itself. The states are made again from the inputs, nothing of the
  * forward is kept. Rows outside every sequence are not written.
