@@ -10,9 +10,15 @@
 //   4. O^T = scale e^G (Q S)^T + U^T P^T
 //   5. S^T = e^{G_C} S^T + (e^{G_C-G} U)^T K
 // Rows behind a sequence's last token are zeros in shared memory and have beta = 0.
-// A CTA is eight warps of one head (four for dv = 64), which share the chunk's K, Q and
-// triangles in two buffers, the next chunk's copies in flight during a chunk.
-// Bound: the latency of a warp's way from product to product, two warps to a sub-core.
+// A forward CTA is eight warps of one head (four, where two CTAs fit an SM or dv is 64), which
+// share the chunk's K, Q and triangles in two buffers, the next chunk's copies in flight during
+// a chunk (d = 128, 256 heads of 2048 tokens: 355 us by eight warps, 403 by four; dk = 64, dv =
+// 128, 256 heads of 1024: 135 by eight, 126 by four). A backward CTA has four warps of each
+// chain (64 heads of 4096 tokens: 394 us, by eight warps of one or the other 452; 128 heads of
+// 1024 of dk = 128, dv = 64: 101, by four of one or the other 126).
+// Bound: the latency of a warp's way from product to product, two warps to a sub-core; the
+// tensor pipe has 73 % of the forward's time (504 products of 16 x 8 x 16 a chunk and 16 columns
+// of d = 128) and 52 % of the backward's (800).
 #include "la_gated_mma.cuh"
 
 namespace la {
@@ -75,7 +81,11 @@ template <int DK, int MODE, int W>
 __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps, long long block, uint8_t* smem) {
   using L = ChainSmem<DK, MODE, W>;
   constexpr int NT = 32 * W, KS = DK / 16;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = MODE == kFwd ? threadIdx.x : threadIdx.x % NT, lane = tid & 31, warp = tid >> 5;
+  auto sync = [] {                                   // of the chain's warps
+    if constexpr (MODE == kFwd) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"n"(MODE), "n"(NT) : "memory");
+  };
   const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, ml = lane & 7;
   const int blk = (int)(block % p.nblk);
   block /= p.nblk;
@@ -153,7 +163,7 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
 
   for (int i = 0; i < nchunks; ++i) {
     const int c = chunk_of(i), t0 = c * C, cn = min(C, n - t0);
-    if (i == 0) __syncthreads();                     // the barriers are there
+    if (i == 0) sync();                              // the barriers are there
     if (!mbar_drain(&bars[i & 1], (i >> 1) & 1, kWaitNs)) *gave_up = 1;
     if (cn < C) {                                    // copies have whole boxes: rows behind the last become zeros
       uint8_t* to = smem + (i & 1) * L::STAGE;
@@ -162,7 +172,7 @@ __device__ __forceinline__ void chain(const ChainArgs& p, const ChainMaps& maps,
           *reinterpret_cast<uint4*>(to + x * C * 128 + cn * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
       sm100::fence_proxy_async_smem();               // (copies come here again)
     }
-    __syncthreads();                                 // the copies are there; the other buffer's readers are done
+    sync();                                          // the copies are there; the other buffer's readers are done
     if (*gave_up) {
       mbar_drain(&bars[i & 1], (i >> 1) & 1, kWaitNs / 8);
       if (tid == 0) atomicExch(p.status, (int)LA_ERR_TIMEOUT);
@@ -543,22 +553,28 @@ gated_chain_kernel(const ChainArgs p, const __grid_constant__ ChainMaps maps) {
   chain<DK, kFwd, W>(p, maps, blockIdx.x, smem);
 }
 
-// Both chains of the backward in one launch (they need nothing of each other; order:
-// second_chain).
-template <int DK, int W>
-__global__ void __launch_bounds__(32 * W)
+// Both chains of the backward of the same columns side by side in a CTA (they need nothing
+// of each other): four warps each.
+template <int DK>
+struct ChainsSmem {
+  static constexpr int SAVE = (ChainSmem<DK, kRev, 4>::TOTAL + 1023) / 1024 * 1024;
+  static constexpr int TOTAL = SAVE + ChainSmem<DK, kSave, 4>::TOTAL;
+  static_assert(TOTAL <= 227 * 1024, "shared memory");
+};
+template <int DK>
+__global__ void __launch_bounds__(256)
 gated_chains_kernel(const ChainArgs rev, const __grid_constant__ ChainMaps rmaps, const ChainArgs save,
                     const __grid_constant__ ChainMaps smaps) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  unsigned number;
-  if (second_chain(blockIdx.x, gridDim.x, rev.offsets != nullptr, rev.nblk * rev.H, number)) chain<DK, kSave, W>(save, smaps, number, smem);
-  else chain<DK, kRev, W>(rev, rmaps, number, smem);
+  if (threadIdx.x < 128) chain<DK, kRev, 4>(rev, rmaps, blockIdx.x, smem);
+  else chain<DK, kSave, 4>(save, smaps, blockIdx.x, smem + ChainsSmem<DK>::SAVE);
 }
 
+// W: of the forward
 template <int DK, int W>
 cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
-  f.nblk = a.dv / (16 * W);
-  const long long grid = (long long)f.nseq * f.H * f.nblk * (save != nullptr ? 2 : 1);
+  f.nblk = a.dv / (16 * (save != nullptr ? 4 : W));
+  const long long grid = (long long)f.nseq * f.H * f.nblk;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const long long keys = (long long)a.B * a.Hk, heads = (long long)a.B * a.H;
   ChainMaps m, ms;
@@ -581,12 +597,11 @@ cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
     b.stall = f.stall;
     ms = m;
     if (!gated_map(&ms.v, b.v, heads, a.N, a.dv, 64)) return cudaErrorInvalidValue;
-    auto kern = gated_chains_kernel<DK, W>;
-    constexpr int smem = ChainSmem<DK, kRev, W>::TOTAL;
-    static_assert(smem >= ChainSmem<DK, kSave, W>::TOTAL, "the reverse chain has more");
+    auto kern = gated_chains_kernel<DK>;
+    constexpr int smem = ChainsSmem<DK>::TOTAL;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)grid, 32 * W, smem, a.stream>>>(f, m, b, ms);
+    kern<<<(unsigned)grid, 256, smem, a.stream>>>(f, m, b, ms);
   }
   e = cudaGetLastError();
   if (e == cudaSuccess) note_launch();
@@ -594,8 +609,8 @@ cudaError_t launch(const GatedArgs& a, ChainArgs f, const ChainArgs* save) {
 }
 
 cudaError_t dispatch(const GatedArgs& a, const ChainArgs& f, const ChainArgs* save) {
-  if (a.dv == 128) return a.dk == 64 ? launch<64, 8>(a, f, save) : launch<128, 8>(a, f, save);
-  return a.dk == 64 ? launch<64, 4>(a, f, save) : launch<128, 4>(a, f, save);
+  if (a.dk == 64) return launch<64, 4>(a, f, save);
+  return a.dv == 128 ? launch<128, 8>(a, f, save) : launch<128, 4>(a, f, save);
 }
 
 ChainArgs chain_args(const GatedArgs& a, const uint8_t* rec, int rec_bytes) {

@@ -25,7 +25,7 @@
 // way from load to product to product of one CTA of 16 warps per SM, which goes through the
 // chunks; a key head's heads of values follow each other, so that dQ and dK of shared heads
 // are summed in registers, in a fixed order. The states come in pieces of 64 values, the
-// next head's while N and W are multiplied; its rows take the place of N and W.
+// next head's while N and W are multiplied; its rows then take the place of N and W.
 #include "la_gated_mma.cuh"
 
 namespace la {
@@ -59,15 +59,17 @@ struct GradSmem {
   // a piece of a state: 64 values of its high and of its low part, rows dv
   static constexpr int PART = (DK / 64) * 8192, PIECE = 2 * PART;
   static constexpr int NP = 2 * (DV / 64);           // pieces a head: S_0, dS, S_0, dS
-  // over a head's rows after step 2: [N; W] high and low, [N; W] beta high and low, the rows' sums
-  static constexpr int TILE = 16384, SUMS = 4 * TILE, WSIZE = SUMS + 4096;
+  // over a head's rows after step 2: [N; W] high and low, [N; W] beta high and low
+  static constexpr int TILE = 16384, WSIZE = 4 * TILE;
   static constexpr int KQ = 0;
   static constexpr int ROWS = KQ + KQB;
   static constexpr int PIECES = ROWS + (ROWB > WSIZE ? ROWB : WSIZE);
-  static constexpr int REST = 5 * C * 4 + 128;       // e^G, e^{G_C-G}, beta, G high and low; control
+  static constexpr int VECB = 5 * C * 4;             // e^G, e^{G_C-G}, beta, G high and low; two heads'
+  static constexpr int REST = 4096 + 2 * VECB + 128;
   static constexpr int SLOTS = PIECES + NP * PIECE + REST <= 227 * 1024 ? NP : 3;
-  static constexpr int VECS = PIECES + SLOTS * PIECE;
-  static constexpr int CTRL = VECS + 5 * C * 4;      // barriers, tensor memory's address, a flag, 16 sums
+  static constexpr int SUMS = PIECES + SLOTS * PIECE;         // the rows' sums
+  static constexpr int VECS = SUMS + 4096;
+  static constexpr int CTRL = VECS + 2 * VECB;       // barriers, tensor memory's address, a flag, 16 sums
   static constexpr int TOTAL = CTRL + 128;
   // columns of tensor memory: dR hi and dO, dR lo times S_0; E dS^T; the same two times E; step 3
   static constexpr int D1 = 0, D1B = 128, D2 = 256, D3 = 384, D3B = 448, D5A = 384, D5B = 128;
@@ -136,20 +138,21 @@ gated_grads_tc_kernel(const GradArgs p) {
     }
     return x;
   };
-  auto load_rows = [&](const Unit& x, int hh) {
-    if (hh == 0) {
-      const long long r = (((long long)x.b * p.Hk + x.hk) * p.N + x.row) * DK;
-      load_box<KCH>(base + L::KQ, 0, L::KBOX, p.k + r, x.n, tid);
-      load_box<KCH>(base + L::KQ, 64, L::KBOX, p.q + r, x.n, tid);
-    }
+  auto load_keys = [&](const Unit& x) {
+    const long long r = (((long long)x.b * p.Hk + x.hk) * p.N + x.row) * DK;
+    load_box<KCH>(base + L::KQ, 0, L::KBOX, p.k + r, x.n, tid);
+    load_box<KCH>(base + L::KQ, 64, L::KBOX, p.q + r, x.n, tid);
+    cp_commit();
+  };
+  auto load_rows = [&](const Unit& x, int hh, int buf) {
     const int h = x.hk * group + hh;
     const long long r = (((long long)x.b * p.H + h) * p.N + x.row) * DV;
     const __nv_bfloat16* const src[5] = {p.c.e, p.c.e_lo, p.c.dr_lo, p.dr, p.dout};
 #pragma unroll
     for (int i = 0; i < 5; ++i) load_box<VCH>(base + L::ROWS, 64 * i, L::RBOX, src[i] + r, x.n, tid);
     const uint8_t* rec = p.rec + ((long long)x.slot * p.H + h) * REC_BWD;
-    load_bytes<VEC, NT>(base + L::VECS, rec + OFF_VEC, tid);
-    load_bytes<2 * C * 4, NT>(base + L::VECS + VEC, rec + OFF_SUMS, tid);
+    load_bytes<VEC, NT>(base + L::VECS + buf * L::VECB, rec + OFF_VEC, tid);
+    load_bytes<2 * C * 4, NT>(base + L::VECS + buf * L::VECB + VEC, rec + OFF_SUMS, tid);
     cp_commit();
   };
   // piece j of a head (S_0 or dS, values 64 (j / 2) ..), in slot (turn + j) % SLOTS
@@ -172,7 +175,8 @@ gated_grads_tc_kernel(const GradArgs p) {
   Unit x = unit_at(blockIdx.x);
   if (x.u >= p.units) return;
   int hh = 0;
-  load_rows(x, 0);
+  load_keys(x);
+  load_rows(x, 0, 0);
   for (int j = 0; j < FIRST; ++j) load_piece(x, 0, 0, j);
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
@@ -189,10 +193,9 @@ gated_grads_tc_kernel(const GradArgs p) {
 
   const int quad = warp & 3, part = warp >> 2, row = 32 * quad + lane;
   const bool kside = quad < 2;                       // rows of dK; else of dQ
+  const bool issuer = tid == NT - 32;                // of products: a thread of the side with fewer results to read
   const int t = row & 63;
   const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-  const float* vec = reinterpret_cast<const float*>(smem + L::VECS);
-  const float *EG = vec, *EC = vec + C, *BT = vec + 2 * C, *GS = vec + 3 * C, *GL = vec + 4 * C;
   uint8_t* wt = smem + L::ROWS;
   float acc[HC];
   bool ok = true;
@@ -238,10 +241,20 @@ gated_grads_tc_kernel(const GradArgs p) {
   };
   while (true) {
     const uint32_t parity = nhead & 1;
+    const float* vec = reinterpret_cast<const float*>(smem + L::VECS + parity * L::VECB);
+    const float *EG = vec, *EC = vec + C, *BT = vec + 2 * C, *GS = vec + 3 * C, *GL = vec + 4 * C;
+    // the next head, or the next chunk's first
+    Unit nx = x;
+    int nh = hh + 1;
+    if (nh == group) {
+      nx = unit_at(x.u + gridDim.x);
+      nh = 0;
+    }
+    const bool more = nx.u < p.units;
     cp_wait<0>();
     fence_proxy_async_smem();
     __syncthreads();
-    if (tid == 0) {
+    if (issuer) {
       tc_fence_after();
       if (FIRST < L::NP) {                           // its slot is wanted first
         products(0);
@@ -262,23 +275,19 @@ gated_grads_tc_kernel(const GradArgs p) {
       }
       tc_commit(&bars[0]);
       // 2. with the states
-      for (int j = FIRST < L::NP ? 1 : 0; j < FIRST; ++j) products(j);
-      if (FIRST == L::NP) tc_commit(&bars[1]);
+      if (FIRST == L::NP) {
+        for (int j = 0; j < FIRST; ++j) products(j);
+        tc_commit(&bars[1]);
+      }
     }
     float dot0 = dot_of(0);
     if (FIRST < L::NP) {
       ok = ok && mbar_wait(&bars[3], parity, abort_flag, kWaitNs);
       __syncthreads();                               // (all have read it, too)
       load_piece(x, hh, turn, FIRST);
+      if (issuer)
+        for (int j = 1; j < FIRST; ++j) products(j);
     }
-    // the next head, or the next chunk's first
-    Unit nx = x;
-    int nh = hh + 1;
-    if (nh == group) {
-      nx = unit_at(x.u + gridDim.x);
-      nh = 0;
-    }
-    const bool more = nx.u < p.units;
     // N or W of this row, columns j = 16 part ..
     const float eg = EG[t], ec = EC[t], bt = BT[t], gs = GS[t], gl = GL[t];
     float nw[16];
@@ -308,7 +317,7 @@ gated_grads_tc_kernel(const GradArgs p) {
       cp_wait<0>();
       fence_proxy_async_smem();
       __syncthreads();
-      if (tid == 0) {
+      if (issuer) {
         products(FIRST);
         tc_commit(&bars[1]);
       }
@@ -370,7 +379,7 @@ gated_grads_tc_kernel(const GradArgs p) {
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (tid == 0) {
+    if (issuer) {
       // 3. [N; W] beta K and [N; W]^T [K; Q]: tokens are the sum's index
       tc_fence_after();
       constexpr uint32_t id = make_idesc_bf16(128, DK, false, true), idt = make_idesc_bf16(128, DK, true, true);
@@ -394,10 +403,11 @@ gated_grads_tc_kernel(const GradArgs p) {
     if (kside) against(L::D2, f3, d3);
     ok = ok && mbar_wait(&bars[2], parity, abort_flag, kWaitNs);
     tc_fence_after();
+    if (more) load_rows(nx, nh, parity ^ 1);         // over N and W
     against(L::D5A, 1.f, d2);
     if (kside) against(L::D5B, bt, d5);
     tc_fence_before();
-    float* sums = reinterpret_cast<float*>(wt + L::SUMS);      // [quarter][f1 d1 + d2 of both sides, d3, d5]
+    float* sums = reinterpret_cast<float*>(smem + L::SUMS);      // [quarter][f1 d1 + d2 of both sides, d3, d5]
     sums[part * 256 + row] = fmaf(f1, d1, d2);
     if (kside) {
       sums[part * 256 + 128 + t] = ec * d3;
@@ -406,11 +416,11 @@ gated_grads_tc_kernel(const GradArgs p) {
     // a wait that gave up: nobody stores, all leave
     if (!__syncthreads_and(ok)) break;
     const int n = x.n;
-    // dQ and dK by way of shared memory (over N and W), so that a warp stores whole rows
+    // dQ and dK by way of shared memory (over K and Q), so that a warp stores whole rows
     if (hh == group - 1) {
 #pragma unroll
       for (int i = 0; i < HC / 8; ++i)
-        *reinterpret_cast<uint4*>(wt + box_at(row, part * (HC / 8) + i, 16384)) =
+        *reinterpret_cast<uint4*>(smem + L::KQ + box_at(row, part * (HC / 8) + i, L::KBOX)) =
             make_uint4(pack2(acc[8 * i], acc[8 * i + 1]), pack2(acc[8 * i + 2], acc[8 * i + 3]),
                        pack2(acc[8 * i + 4], acc[8 * i + 5]), pack2(acc[8 * i + 6], acc[8 * i + 7]));
       __syncthreads();
@@ -461,12 +471,12 @@ gated_grads_tc_kernel(const GradArgs p) {
         const int r = i / KCH, c = i % KCH;
         if ((r & 63) < n)
           *reinterpret_cast<uint4*>((r < 64 ? p.dk : p.dq) + at + (r & 63) * DK + c * 8) =
-              *reinterpret_cast<const uint4*>(wt + box_at(r, c, 16384));
+              *reinterpret_cast<const uint4*>(smem + L::KQ + box_at(r, c, L::KBOX));
       }
     }
     if (!more) break;
-    __syncthreads();                                 // the sums, the rows on their way out and K, Q have been read
-    load_rows(nx, nh);
+    __syncthreads();                                 // the sums and the rows on their way out have been read
+    if (nh == 0) load_keys(nx);
     x = nx; hh = nh;
     turn += L::NP;
     ++nhead;
@@ -474,7 +484,7 @@ gated_grads_tc_kernel(const GradArgs p) {
   // copies and products in flight end before shared and tensor memory are released
   cp_wait<0>();
   if (*abort_flag) {
-    if (tid == 0) {
+    if (issuer) {
       mbar_init(&bars[4], 1);
       fence_mbar_init();
       tc_commit(&bars[4]);
