@@ -11,18 +11,15 @@
 // and leaves S's and U's fragments in shared memory for its helper warp, which a
 // chunk later does what the chain need not wait for:
 //   5. O^T = scale e^G (Q S)^T + U^T P^T, the outputs
-// and the copies of later chunks, by TMA (by cp.async, 26 a thread and chunk: 342 us in the
-// place of 316 for the packed prompts below). A CTA is four pairs of one head that share a chunk's
+// and the copies of later chunks, by TMA (by cp.async, 26 a thread and chunk, a twelfth more). A CTA is four pairs of one head that share a chunk's
 // K, Q and triangles; a pair's warps share a sub-core, whose tensor pipe has the helper's
 // products while the chain warp goes from one product to the next. One barrier a chunk.
 // Rows behind a sequence's last token are zeros in shared memory and have beta = 0.
 //
-// What bounds it: without a state asked for, shared memory, which passes 3200 of a chunk's
-// 3600 cycles (every 16 x 16 block of K, Q, T, P is read for two products of 16 cycles in all, so that
-// at the tensor pipe's rate it would be as busy; a warp with 32 columns halves the reads but
-// has no second warp beside it: 258 us in the place of 242 at 256 heads of 2048 tokens, 362
-// in the place of 121 at 64 of 4096). With one, where a block is read for four products,
-// the tensor pipe: 63 % of the time.
+// What bounds it: the tensor pipe has 2.0 of a chunk's 2.9 us at d = 128 (504 products of
+// 16 x 8 x 16 a chunk and 16 columns, two warps to a sub-core), the rest is the chain warp's way
+// from product to product. (A warp with 32 columns halves the reads of K, Q, T and P but has
+// no second warp beside it, and was slower at every size.)
 #include "la_gated_mma.cuh"
 
 namespace la {
@@ -461,10 +458,10 @@ cudaError_t launch(PairArgs p, const PairMaps& maps, cudaStream_t stream) {
 
 }  // namespace
 
-// d = 128: 64 heads of 4096 tokens (128 CTAs) 121 us against 141 by one warp for 16 columns,
-// with a state 154 against 195; 256 heads of 2048 (512 CTAs here, 256 there) 242 against 227, with a state 309
-// against 314; d = 64, 1024 heads of 1024: 166 against 141. Packed, 32 heads of twelve sequences
-// with one of half the rows: 247 against 317, with a state 310 against 427.
+// d = 128: 64 heads of 4096 tokens (128 CTAs) 189 us against 352 by one warp for 16 columns;
+// 80 heads (160) 373 against 354, 256 heads of 2048 (512) 376 against 355; d = 64, 1024
+// heads of 1024: 239 against 214. Packed, 16384 rows, 32 heads: of twelve unlike sequences
+// 342 against 356, of 40 like ones 428 against 399.
 bool gated_pair_wanted(const GatedArgs& a) {
   return a.offsets != nullptr || (long long)a.nseq * a.H * (a.dv / (16 * W)) <= kSlots;
 }

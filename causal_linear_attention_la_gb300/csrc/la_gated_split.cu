@@ -795,17 +795,21 @@ bool gated_map(CUtensorMap* m, const void* ptr, long long heads, int N, int d, i
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// One of these CTAs has an SM for itself and takes 1.0 us a chunk of d = 128, 1.15 with a
-// state asked for; pairs of warps take 1.9 and 2.4, but four share an SM. 16 heads of 4096 tokens
-// (128 CTAs here): 64 us against 121, with a state 74 against 153; 32 heads (256): 127
-// against 121, 148 against 154; 64 heads (512): 252 against 121. Packed sequences are taken to have
-// one of half their rows: 16 heads 238 against 249, with a state 283 against 315; 32 heads 472 against
-// 247; backward, 16 heads of one sequence of 4096 tokens 143 against 158 by the chains of la_gated_chain.cu, 24 heads
-// 199 against 158.
+// One of these CTAs has an SM for itself and takes 1.3 us a chunk of d = 128 (backward, the
+// reverse chain and the one that keeps the states, 1.4 each); pairs of warps take 2.9, but four
+// share an SM, and both chains of four column groups of the backward 6.1 (d = 64: 4.3). 4096
+// tokens of d = 128, forward: 16 heads (128 CTAs here) 81 us against 188, 32 heads 166 against
+// 188, 64 heads 330 against 189; backward: 19 heads (304) 179 against 390, 32 heads 349 against
+// 390, 64 heads 625 against 394; 1024 tokens, d = 64, 256 heads (2048) 289 against 137. Packed
+// sequences are taken to have one of half their rows, of more than eight one of 4 / nseq of
+// them: 16 heads of 16384 rows, 12 unlike ones, 308 against 190, 40 like ones 449 against 226;
+// backward of 12 heads of 8192 rows, d = 64, nine unlike ones 116 against 222, 40 like ones
+// 233 against 81.
 bool gated_split_wanted(const GatedArgs& a, bool backward) {
   const long long groups = (long long)a.H * (a.dv / 16) * (backward ? 2 : 1);
-  const long long together = a.offsets != nullptr && a.nseq > 2 ? 2 : a.nseq;
-  return groups * together <= 2 * kSlots;
+  const long long most = (backward ? a.dk == 128 ? 4 : 3 : 2) * kSlots;
+  if (a.offsets == nullptr || a.nseq <= 2) return groups * a.nseq <= most;
+  return groups * (a.nseq > 8 ? a.nseq : 8) <= 4 * most;
 }
 
 cudaError_t gated_split_forward(const GatedArgs& a, const uint8_t* records) {
