@@ -70,9 +70,11 @@ la_status check_call(const char* who, const GatedArgs& a, bool backward, bool* e
   return LA_OK;
 }
 
-// Whole sequences on the tensor cores; N <= kShortN tokens are read token by token:
-// 16 heads of 8, 32, 48 tokens 5, 13, 15 us against 12 on the tensor cores, 256 heads 12,
-// 34, 58 against 29.
+// Whole sequences on the tensor cores; N <= kShortN tokens are read token by token. Forward:
+// 16 heads of 8, 16, 32, 48 tokens 5, 7, 12, 15 us against 12 on the tensor cores, 256 heads
+// 10, 17, 32, 56 against 23. Backward: 16 heads of 8, 32 tokens 41, 54 against 28, 256 heads
+// 96, 155 against 61, 67; but of so few tokens without a state dg is mostly what cancels (a first
+// token's all of it, to exactly zero in this path, to what rounding leaves of the terms in the other).
 constexpr int kShortN = 32;
 bool use_mma(int N, int dk, int dv, la_dtype dtype) {
   return N > kShortN && current_path() == LA_PATH_AUTO && gated_on_tensor_cores(dk, dv, dtype);

@@ -94,7 +94,7 @@ __device__ __forceinline__ Pair log2_pair(float g) {
 }
 
 template <int DK, bool kBackward>
-__global__ void __launch_bounds__(PT, 4)          // (five CTAs an SM, with spills: 89 us for 83)
+__global__ void __launch_bounds__(PT, 4)          // (256 heads of 2048 tokens 121 us; three CTAs an SM 135, five 125)
 gated_prep_kernel(const PrepArgs p) {
   extern __shared__ __align__(16) uint8_t raw[];
   PrepSmem<DK>& sm = *reinterpret_cast<PrepSmem<DK>*>(raw);

@@ -535,7 +535,8 @@ LA_API la_status la_state_unpack(const unsigned char* codes, const unsigned char
  * product go in as bf16 high and low parts (states within 1e-5 of their 2-norm on unit-norm
  * keys in random directions, within 3e-5 on keys that are nearly equal; outputs and gradients
  * within bf16's rounding of these; dg, whose terms cancel the most, within 2^-18 of the terms
- * it is a sum of). Otherwise, and for N <= 32, token by token in fp32. The tensor core kernels' waits are bounded:
+ * it is a sum of). Otherwise, and for N <= 32, token by token in fp32 (with la_set_path(
+ * LA_PATH_SIMT) every call: states then are fp32's). The tensor core kernels' waits are bounded:
  * la_device_status has LA_ERR_TIMEOUT if one ever ran out.
  */
 LA_API int la_gated_delta_path(int dk, int dv, la_dtype dtype);

@@ -71,3 +71,15 @@ def test_waits_give_up_and_the_next_call_runs(size, gradients):
     torch.cuda.synchronize()
     assert la.la_device_status(True) == la.LA_OK
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("N", [1, 2, 7, 16, 32])
+@pytest.mark.parametrize("H, dk, dv", [(4, 128, 128), (64, 64, 64), (2, 64, 128), (80, 128, 64)])
+def test_gradients_of_short_sequences(H, dk, dv, N):
+    dev, do, S0, dS = inputs(H, N, dk, dv)
+    got = la.backward_gated_delta(*dev, do, S0=S0, dS=dS)
+    x = [to_host(y)[:, :1 if i < 2 else 2] for i, y in enumerate(dev)]
+    want = gated.backward(*x, to_host(do)[:, :2], dk ** -0.5, to_host(S0)[:, :2], to_host(dS)[:, :2])
+    for name, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "dS0"), got, want):
+        a = to_host(a)[:, :1 if name in ("dq", "dk") else 2]
+        assert np.linalg.norm(a - b) <= (2.0 ** -15 if name == "dS0" else 2.0 ** -8) * np.linalg.norm(b), name

@@ -94,3 +94,18 @@ def test_large_beta_and_positive_decay(heads):
     got = la.backward_gated_delta(*dev, do)
     for x, y in zip(got, gated.backward(*host, to_host(do)[:, some], d ** -0.5)):
         assert np.linalg.norm(to_host(x)[:, some] - y) <= 2.0 ** -7 * np.linalg.norm(y)
+
+
+def test_gradients_beyond_32_bits():
+    """17 million rows of 256 bytes, 262146 chunks' states of 32 KiB: the last sequence's
+    gradients as by itself."""
+    n, tail, d = (1 << 24) + 70, 150, 128
+    dev, _, _, do, _ = inputs(1, tail, d, seed=8)
+    want = la.backward_gated_delta(*dev, do)
+    big = [torch.zeros(x.shape[:2] + (n,) + x.shape[3:], dtype=x.dtype, device="cuda") for x in dev + [do]]
+    for x, y in zip(big, dev + [do]):
+        x[:, :, n - tail:] = y
+    off = torch.tensor([0, n - tail, n], dtype=torch.int32, device="cuda")
+    got = la.backward_gated_delta(*big[:5], big[5], offsets=off)
+    for x, y in zip(got, want):
+        assert torch.equal(x[:, :, n - tail:], y) and not x[:, :, :n - tail].any()
