@@ -82,16 +82,16 @@ bool use_mma(int N, int dk, int dv, la_dtype dtype) {
 
 bool packed_size(int B, int nseq) { return B == 1 && nseq != 1; }
 
-// Strides of rows [B][N][heads][d]; where they are written, no two rows may
-// start at the same place.
-la_status check_strides(const char* who, const char* name, const long long* s, int size, const int* written) {
+// Strides of rows [B][N][heads][d]; where they are written, no row may begin inside its
+// neighbour.
+la_status check_strides(const char* who, const char* name, const long long* s, int size, const int* written, int d) {
   if (s == nullptr) return fail(LA_ERR_INVALID_ARG, "%s: %s must be non-NULL", who, name);
   const int per = 16 / size;
   for (int i = 0; i < 3; ++i)
     if (s[i] < 0 || s[i] % per != 0 || s[i] > (1LL << 40))
       return fail(LA_ERR_INVALID_ARG, "%s: %s must be non-negative multiples of 16 bytes", who, name);
   for (int i = 0; i < 3 && written != nullptr; ++i)
-    if (written[i] > 1 && s[i] == 0) return fail(LA_ERR_INVALID_ARG, "%s: %s of written rows must not be 0", who, name);
+    if (written[i] > 1 && s[i] < d) return fail(LA_ERR_INVALID_ARG, "%s: %s of written rows must not be below d=%d", who, name, d);
   return LA_OK;
 }
 
@@ -124,8 +124,8 @@ la_status norm_call(const char* who, NormArgs& a, int norm, const long long* con
     if (!aligned(a.x[i], 16) || !aligned(a.y[i], 16) || !aligned(a.dy[i], 16) || !aligned(a.dx[i], 16))
       return fail(LA_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", who);
     const int extent[3] = {a.B, a.N, a.H[i]};
-    la_status st = check_strides(who, i ? "k_stride" : "q_stride", stride[i], size, nullptr);
-    if (st == LA_OK && backward) st = check_strides(who, i ? "dk_stride" : "dq_stride", dstride[i], size, extent);
+    la_status st = check_strides(who, i ? "k_stride" : "q_stride", stride[i], size, nullptr, a.d);
+    if (st == LA_OK && backward) st = check_strides(who, i ? "dk_stride" : "dq_stride", dstride[i], size, extent, a.d);
     if (st != LA_OK) return st;
     for (int j = 0; j < 3; ++j) {
       a.stride[i][j] = stride[i][j];

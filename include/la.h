@@ -528,12 +528,13 @@ LA_API la_status la_state_unpack(const unsigned char* codes, const unsigned char
  *         graphs too.
  * A token's row reaches no token before it and no other sequence, whatever
  * it holds. dk, dv in {16, 32, 64, 128}; N * B, and chunks of 32 tokens times H,
- * up to 2^31 - 1. Nothing is joined by atomics: results repeat bit for bit.
+ * up to 2^31 - 1. Nothing is joined by atomics: results repeat bit for bit. Outputs overlap no
+ * input but where that is said.
  *
  * Where la_gated_delta_path is 1 (bf16, dk and dv in {64, 128}) whole sequences
  * are computed in chunks of 64 tokens on the tensor cores; fp32 operands of a
  * product go in as bf16 high and low parts (states within 1e-5 of their 2-norm on unit-norm
- * keys in random directions, within 3e-5 on keys that are nearly equal; outputs and gradients
+ * keys in random directions, within 3e-5 on keys that are nearly equal, dS0 within 4e-5; outputs and gradients
  * within bf16's rounding of these; dg, whose terms cancel the most, within 2^-18 of the terms
  * it is a sum of). Otherwise, and for N <= 32, token by token in fp32 (with la_set_path(
  * LA_PATH_SIMT) every call: states then are fp32's). The tensor core kernels' waits are bounded:
@@ -612,7 +613,8 @@ LA_API la_status la_clear_outside(void* const* rows, const int* row_bytes, const
  * positions [B,N] int32 or NULL (0 .. N-1; any value is allowed, negative too)
  * freqs     [rot/2] fp32, finite; NULL if rot = 0
  * d in {16, 32, 64, 128}; rot a multiple of 16, 0 .. d. Hk = 0 (k, k_out NULL) or
- * Hq = 0 norms the other alone. A row of zeros with eps = 0 gives NaN, as the formula.
+ * Hq = 0 norms the other alone. Sums are fp32: a row of zeros with eps = 0 gives NaN, as the
+ * formula; one whose sum of squares passes fp32's range gives zeros. Outputs do not overlap inputs.
  */
 enum { LA_NORM_RMS = 0, LA_NORM_L2 = 1 };
 LA_API la_status la_qk_norm_rotate(const void* q, const void* k, const float* q_weight, const float* k_weight,
@@ -624,7 +626,7 @@ LA_API la_status la_qk_norm_rotate(const void* q, const void* k, const float* q_
 /*
  * Gradients of la_qk_norm_rotate: dq_out, dk_out as q_out, k_out; dq, dk_ are
  * rows at strides dq_stride, dk_stride, as q and k (slices of a fused
- * gradient, not overlapping anything else); dq_weight, dk_weight [d] fp32 out, given where the weight
+ * gradient, not overlapping anything else; a stride below d is refused); dq_weight, dk_weight [d] fp32 out, given where the weight
  * is (NULL: not wanted). Sums over tokens and heads in fp32, in a fixed order.
  */
 LA_API size_t la_qk_norm_rotate_backward_workspace_size(int B, int N, int Hq, int Hk, int d, la_dtype dtype);
