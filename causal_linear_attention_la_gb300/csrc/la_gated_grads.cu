@@ -21,11 +21,12 @@
 //   3. [N; W] beta K, [N; W]^T [K; Q]
 // (lanes 64-127 of what sums dR's low part, E dS^T and the transposed product are unused).
 //
-// Bound: HBM (272 KB a chunk and head at d = 128, the two states 128 of them) and the
-// way from load to product to product of one CTA of 16 warps per SM, which goes through the
-// chunks; a key head's heads of values follow each other, so that dQ and dK of shared heads
-// are summed in registers, in a fixed order. The states come in pieces of 64 values, the
-// next head's while N and W are multiplied; its rows then take the place of N and W.
+// Bound: HBM (240 KB a chunk and head at d = 128, the two states 128 of them: 150 us for 64
+// heads of 4096 tokens) and the way from load to product to product of one CTA of 16 warps per
+// SM, which goes through the chunks (276 us; the products have 5400 of a chunk's 20000 cycles).
+// A key head's heads of values follow each other, so that dQ and dK of shared heads are summed
+// in registers, in a fixed order. The states come in pieces of 64 values, the next head's
+// while N and W are multiplied; its rows then take the place of N and W.
 #include "la_gated_mma.cuh"
 
 namespace la {
